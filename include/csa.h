@@ -403,6 +403,132 @@ csa_status_t lightning_indexer_topk_noalloc(const uint8_t* qI, const float* qI_s
                                             int64_t ld_scores, int32_t* dev_status, void* stream);
 
 /*
+ * The lightning indexer's inputs
+ * ------------------------------
+ * The calls below make what the two indexers read: MXFP4 rows (quantisation, its inverse and
+ * the product of two MXFP4 matrices, for the projections in front of the indexer), query and
+ * key heads with their RMSNorm and position rotation, the query heads in the indexer's
+ * stored format, and the append of entries' indexer keys to the (paged) key store.
+ * Row counts of zero are no-ops.  Pointers to rows are 16-byte aligned and row / head / token
+ * strides (in elements) are multiples of 16 bytes; channels are contiguous.
+ */
+
+/* Element types of rows. */
+#define CSA_DT_BF16 0
+#define CSA_DT_F16 1
+#define CSA_DT_F32 2
+
+/* Layouts of MXFP4 scale bytes.
+ * CSA_SF_ROWS: uint8 [rows, cols / 32], what lightning_indexer_topk_mxfp4 reads.
+ * CSA_SF_TILED: tiles of 128 rows x 4 blocks, 512 bytes each, tile (r / 128, j / 4) at
+ *   512 * ((r / 128) * ceil(cols / 128) + j / 4), block j of row r at byte
+ *   16 * (r % 32) + 4 * (r % 128 / 32) + j % 4 of its tile: the layout the tensor cores'
+ *   scales have, which csa_mxfp4_matmul reads.  Rows and blocks that pad the last tiles
+ *   are written as zeros by csa_mxfp4_quantize; the product needs them finite (not 0xFF). */
+#define CSA_SF_ROWS 0
+#define CSA_SF_TILED 1
+
+/* Stored formats of indexer query heads and keys.
+ * CSA_IDX_FP8: e4m3 codes [.., d] and one fp32 scale per row (absmax / 448, 1 for a zero
+ *   row), as lightning_indexer_topk reads them.
+ * CSA_IDX_MXFP4: packed e2m1 [.., d / 2] and UE8M0 scales [.., d / 32] (CSA_SF_ROWS), as
+ *   lightning_indexer_topk_mxfp4 reads them. */
+#define CSA_IDX_FP8 0
+#define CSA_IDX_MXFP4 1
+
+/*
+ * csa_mxfp4_quantize -- rows to MXFP4 ("DeepSeek-V4 深度分析报告" 3.4; OCP microscaling).
+ *   Per block of 32 consecutive elements, with amax its largest magnitude: the scale is
+ *   2^e, e = floor(log2(amax)) - 2, stored as the byte max(e + 127, 0) (0 for a zero block);
+ *   each element becomes the e2m1 value nearest to x / 2^e, ties to the even code, past 6 to
+ *   6.  A block with an infinity or a NaN gets the scale byte 0xFF (NaN) and zero codes, and
+ *   sets CSA_DEV_NAN.  Exact: the codes do not depend on the batch.
+ * Arguments:
+ *   x [rows, cols] in dtype (CSA_DT_*), row stride ld elements (ld >= cols)
+ *   codes uint8 [rows, cols / 2], element 2j in the low nibble; sf: scale bytes in
+ *   sf_layout, csa_mxfp4_sf_bytes(rows, cols, sf_layout) bytes
+ *   cols: a multiple of 32, up to 2^20
+ *
+ * csa_mxfp4_dequantize -- the values MXFP4 rows stand for, out [rows, cols] in dtype, row
+ *   stride ld (exact in fp32 and bf16; fp16 rounds to nearest and overflows to infinity; a
+ *   block with scale 0xFF gives NaN).
+ *
+ * csa_mxfp4_matmul -- out[m, n] = sum_k A[m, k] B[n, k] on the tensor cores.
+ *   a uint8 [M, K / 2] and b uint8 [N, K / 2] packed e2m1 (say activations and a weight),
+ *   a_sf, b_sf their scales in CSA_SF_TILED; K a multiple of 32, up to 2^20.
+ *   out [M, N] in dtype, row stride ld elements (any ld >= N; out needs the alignment of
+ *   its element type only).  Accumulated in fp32 over k ascending without split-K, rounded once:
+ *   a row's result does not depend on M.  A 0xFF scale makes NaN of the results it enters.
+ * Errors: CSA_ERR_INVALID_ARG, CSA_ERR_UNSUPPORTED, CSA_ERR_CUDA; the product reports
+ * CSA_DEV_TIMEOUT.
+ */
+size_t csa_mxfp4_sf_bytes(int64_t rows, int64_t cols, int32_t sf_layout);
+csa_status_t csa_mxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols,
+                                int64_t ld, uint8_t* codes, uint8_t* sf, int32_t sf_layout,
+                                int32_t* dev_status, void* stream);
+csa_status_t csa_mxfp4_dequantize(const uint8_t* codes, const uint8_t* sf, int32_t sf_layout,
+                                  int64_t rows, int64_t cols, void* out, int32_t dtype,
+                                  int64_t ld, void* stream);
+csa_status_t csa_mxfp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b,
+                              const uint8_t* b_sf, int64_t M, int64_t N, int64_t K, void* out,
+                              int32_t dtype, int64_t ld, int32_t* dev_status, void* stream);
+
+/*
+ * csa_qk_norm_rope -- RMSNorm of every query and key head and the position rotation, in one
+ * pass ("DeepSeek-V4 深度分析报告" "其他注意力技术细节": RMSNorm of queries and KV, partial RoPE).
+ *   y = x / sqrt(mean(x^2) + eps) * weight over the D channels of a head (norm = 0: y = x *
+ *   weight); then the last rope_dims channels are rotated in interleaved pairs at pos[t],
+ *   pair j by pos * theta^(-2j / rope_dims).  fp32 arithmetic, angles in fp64, one rounding.
+ * Arguments:
+ *   q, k, q_out, k_out: [T, heads, D] in dtype, element strides *_st between tokens and *_sh
+ *   between heads; q has H heads, k has Hk (either may be NULL with 0 heads).  An output may
+ *   be its own input (same pointer and strides); otherwise outputs overlap nothing.
+ *   q_weight, k_weight: fp32 [D], nullable (ones), 16-byte aligned; pos int32 [T]
+ *   D: a multiple of 8 up to 1024; rope_dims: even, 0 .. min(D, 128)
+ *   (sparse_mqa_attn and dense_hca_attn rotate their queries themselves: rope_dims = 0 makes
+ *   their input.)
+ *
+ * csa_indexer_queries -- the same norm and rotation of the indexer's query heads, quantised.
+ *   q [Q, H, D] in dtype (strides q_st, q_sh), q_pos int32 [Q]; codes and scale contiguous
+ *   [Q, H, ..] in fmt (CSA_IDX_*; scale: fp32 [Q, H], or UE8M0 [Q, H, D / 32] bytes).
+ *   D 64 or 128; rope_dims a multiple of 8, 0 .. D.  Computed in fp64 up to the rounding to
+ *   codes, which are those of the definition whatever the batch.  A row (FP8) or block
+ *   (MXFP4) that is not finite, or past the scale's range, gets a NaN scale and zero codes
+ *   and sets CSA_DEV_NAN.
+ *
+ * csa_indexer_append -- indexer keys of listed entries into the key store.
+ *   Key n (row n of k [n_items, D], row stride k_ld) belongs to entry item_ent[n] of sequence
+ *   item_seq[n]; it is normed, rotated at the entry's block-end position (i + 1) * m - 1,
+ *   quantised as by csa_indexer_queries and written to the entry's row of codes [ent_rows,
+ *   ..] and scale [ent_rows, ..] (block table of the layout, or ent_off).  Any number of
+ *   entries per sequence, in any order; only the listed rows are written.  An entry listed
+ *   twice must carry the same key.  A sequence >= B, an entry whose block has not ended
+ *   ((i + 1) * m > seq_len[b]) or a row outside ent_rows sets CSA_DEV_OOB and is not written.
+ *   csa_cache_append (kI_new = NULL) and csa_compress fill the rest of the cache.
+ * Errors (all three): CSA_ERR_INVALID_ARG, CSA_ERR_UNSUPPORTED, CSA_ERR_CUDA.
+ */
+csa_status_t csa_qk_norm_rope(const void* q, int64_t q_st, int64_t q_sh, const void* k,
+                              int64_t k_st, int64_t k_sh, const int32_t* pos,
+                              const float* q_weight, const float* k_weight, void* q_out,
+                              int64_t qo_st, int64_t qo_sh, void* k_out, int64_t ko_st,
+                              int64_t ko_sh, int32_t dtype, int32_t T, int32_t H, int32_t Hk,
+                              int32_t D, int32_t rope_dims, int32_t norm, float rope_theta,
+                              float eps, void* stream);
+csa_status_t csa_indexer_queries(const void* q, int32_t dtype, int64_t q_st, int64_t q_sh,
+                                 const int32_t* q_pos, const float* weight, int32_t norm,
+                                 int32_t rope_dims, float rope_theta, float eps, int32_t Q,
+                                 int32_t H, int32_t D, int32_t fmt, uint8_t* codes, void* scale,
+                                 int32_t* dev_status, void* stream);
+csa_status_t csa_indexer_append(const void* k, int32_t dtype, int64_t k_ld,
+                                const int64_t* seq_len, const int64_t* ent_off,
+                                const int32_t* item_seq, const int32_t* item_ent, int64_t n_items,
+                                int32_t B, int32_t m, const float* weight, int32_t norm,
+                                int32_t rope_dims, float rope_theta, float eps, int32_t D,
+                                int32_t fmt, uint8_t* codes, void* scale, int64_t ent_rows,
+                                const csa_cache_layout_t* layout, int32_t* dev_status,
+                                void* stream);
+
+/*
  * Launch accounting and kernel timing (no counterpart on the pages; instrumentation).
  *   csa_launch_count: kernels this library has launched in the process so far.
  *   csa_profile_enable(1): from now on every launch is bracketed by a CUDA event pair

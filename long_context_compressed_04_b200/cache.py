@@ -11,9 +11,11 @@ management).
 A decode step appends one token per sequence (``csa_cache_append``: ring row, and the
 indexer key of an entry the token completes), compresses the entries completed this step
 from the ring into their blocks (``csa_compress``), selects (``lightning_indexer_topk``) and
-attends (``sparse_mqa_attn``), every call with the same cache layout.  This module keeps the
-host-side bookkeeping (block allocation, the item lists of completed entries); every copy,
-compression, score, selection and attention runs in libcsa.
+attends (``sparse_mqa_attn``), every call with the same cache layout.  Indexer keys come
+ready-made with the token, or as bf16 / fp32 rows that ``append_keys`` norms, rotates and
+quantises on the way into their blocks (``csa_indexer_append``); the key store holds FP8 or
+MXFP4 rows.  This module keeps the host-side bookkeeping (block allocation, the item lists of
+completed entries); every copy, compression, score, selection and attention runs in libcsa.
 """
 from __future__ import annotations
 
@@ -21,8 +23,10 @@ from typing import List, Optional
 
 import torch
 
-from . import (CSA_KV_BF16, cache_layout, csa_cache_append, csa_compress, csa_entry_row_bytes,
-               csa_indexer_workspace_size, lightning_indexer_topk, sparse_mqa_attn)
+from . import (CSA_IDX_FP8, CSA_IDX_MXFP4, CSA_KV_BF16, cache_layout, csa_cache_append,
+               csa_compress, csa_entry_row_bytes, csa_indexer_append,
+               csa_indexer_workspace_size, lightning_indexer_topk,
+               lightning_indexer_topk_mxfp4, sparse_mqa_attn)
 
 BLOCK_TOKENS = 128      # lcm(m, m') of the pages
 M = 4                   # CSA compression ratio
@@ -48,8 +52,13 @@ class HybridCache:
     """Device buffers and bookkeeping of one CSA layer's cache for B decode sequences."""
 
     def __init__(self, B: int, D: int, fmt: int, d_I: int, n_blocks: int, max_blocks: int,
-                 ring: int = 128, device="cuda"):
+                 ring: int = 128, device="cuda", idx_fmt: int = CSA_IDX_FP8):
+        """idx_fmt: the key store's rows, CSA_IDX_FP8 (kI e4m3, ks fp32) or CSA_IDX_MXFP4
+        (kI packed e2m1, ks UE8M0 bytes)."""
+        if idx_fmt not in (CSA_IDX_FP8, CSA_IDX_MXFP4):
+            raise ValueError(f"unknown indexer format {idx_fmt}")
         self.B, self.D, self.fmt, self.d_I, self.ring = B, D, fmt, d_I, ring
+        self.idx_fmt = idx_fmt
         dev = torch.device(device)
         self.device = dev
         rb = csa_entry_row_bytes(fmt, D)
@@ -58,8 +67,12 @@ class HybridCache:
         self.gate = torch.zeros((B * ring, D), dtype=torch.bfloat16, device=dev)
         self.kv_off = torch.arange(B, dtype=torch.int64, device=dev) * ring
         self.entries = torch.zeros((rows, rb), dtype=torch.uint8, device=dev)
-        self.kI = torch.zeros((rows, d_I), dtype=torch.uint8, device=dev)
-        self.ks = torch.zeros(rows, dtype=torch.float32, device=dev)
+        if idx_fmt == CSA_IDX_FP8:
+            self.kI = torch.zeros((rows, d_I), dtype=torch.uint8, device=dev)
+            self.ks = torch.zeros(rows, dtype=torch.float32, device=dev)
+        else:
+            self.kI = torch.zeros((rows, d_I // 2), dtype=torch.uint8, device=dev)
+            self.ks = torch.zeros((rows, d_I // 32), dtype=torch.uint8, device=dev)
         self.block_table = torch.full((B, max_blocks), -1, dtype=torch.int32, device=dev)
         self.bt_host = torch.full((B, max_blocks), -1, dtype=torch.int32)
         self.seq_len = torch.zeros(B, dtype=torch.int64, device=dev)
@@ -91,9 +104,10 @@ class HybridCache:
         self.seq_len[b] = 0
 
     # ---- loading a prefix (set-up) -----------------------------------------------
-    def load_prefix(self, b: int, kv_tail, gate_tail, T: int, entries, kI, ks):
+    def load_prefix(self, b: int, kv_tail, gate_tail, T: int, entries, kI=None, ks=None):
         """Sequence b with T tokens: the last min(T, ring) raw rows (kv_tail, gate_tail, in
-        position order), its T // 4 entry rows, indexer keys and scales (in entry order)."""
+        position order), its T // 4 entry rows, indexer keys and scales (in entry order; None:
+        append_keys brings them)."""
         n = T // M
         self._ensure_blocks(b, n)
         self._push_table()
@@ -105,16 +119,20 @@ class HybridCache:
         rows = (self.bt_host[b, i // BLOCK_ENTRIES].to(torch.int64) * BLOCK_ENTRIES
                 + i % BLOCK_ENTRIES).to(self.device)
         self.entries[rows] = entries
-        self.kI[rows] = kI
-        self.ks[rows] = ks
+        if kI is not None:
+            self.kI[rows] = kI
+            self.ks[rows] = ks
         self.seq_len[b] = T
         self.len_host[b] = T
 
     # ---- one decode step -----------------------------------------------------------
-    def append(self, kv_new, gate_new, kI_new, ks_new, stream=None):
-        """One token per sequence (bf16 [B, D] raw KV and gate; e4m3 [B, d_I] indexer key and
-        fp32 [B] scale, used by the sequences whose token completes an entry).  Returns the
-        (item_seq, item_ent) lists of the entries completed, for compress()."""
+    def append(self, kv_new, gate_new, kI_new=None, ks_new=None, stream=None):
+        """One token per sequence (bf16 [B, D] raw KV and gate; with an FP8 key store, e4m3
+        [B, d_I] indexer key and fp32 [B] scale, used by the sequences whose token completes
+        an entry; None: append_keys brings the keys).  Returns the (item_seq, item_ent) lists
+        of the entries completed, for compress() and append_keys()."""
+        if kI_new is not None and self.idx_fmt != CSA_IDX_FP8:
+            raise ValueError("ready-made keys are copied into an FP8 key store only: use append_keys")
         changed = False
         for b in range(self.B):
             changed |= self._ensure_blocks(b, (self.len_host[b] + 1) // M)
@@ -122,7 +140,8 @@ class HybridCache:
             self._push_table()
         csa_cache_append(kv_new, gate_new, self.seq_len, self.kv_off, None, self.kv, self.gate,
                          B=self.B, D=self.D, m=M, kI_new=kI_new, kI_scale_new=ks_new,
-                         kI=self.kI, kI_scale=self.ks, layout=self.layout,
+                         kI=None if kI_new is None else self.kI,
+                         kI_scale=None if kI_new is None else self.ks, layout=self.layout,
                          dev_status=self.dev_status, stream=stream)
         seqs, ents = [], []
         for b in range(self.B):
@@ -133,6 +152,19 @@ class HybridCache:
         return (torch.tensor(seqs, dtype=torch.int32, device=self.device),
                 torch.tensor(ents, dtype=torch.int32, device=self.device))
 
+    def append_keys(self, items, k, weight=None, norm: bool = True, rope_dims: int = 64,
+                    rope_theta=10000.0, eps=1e-6, stream=None):
+        """Indexer keys of entries already in the cache's sequences: k [n, d_I] (bf16, fp16 or
+        fp32), row j for entry items[1][j] of sequence items[0][j]; normed, rotated at the
+        entries' block ends, quantised and written to their blocks."""
+        seq, ent = items
+        if seq.numel() == 0:
+            return
+        csa_indexer_append(k, self.seq_len, None, seq, ent, self.kI, self.ks, B=self.B, m=M,
+                           fmt=self.idx_fmt, weight=weight, norm=norm, rope_dims=rope_dims,
+                           rope_theta=rope_theta, eps=eps, layout=self.layout,
+                           dev_status=self.dev_status, stream=stream)
+
     def compress(self, items, bias, rope_theta=10000.0, eps=1e-6, stream=None):
         seq, ent = items
         if seq.numel() == 0:
@@ -142,11 +174,21 @@ class HybridCache:
                      eps=eps, layout=self.layout, dev_status=self.dev_status, stream=stream)
 
     def select(self, qI, qs, w, q_seq, q_pos, idx_out, *, H_I: int, k: int,
-               workspace: Optional[torch.Tensor] = None, stream=None):
+               workspace: Optional[torch.Tensor] = None, stream=None,
+               select_bf16: bool = False):
+        """Top-k of every query; qI, qs: e4m3 codes and fp32 scales, or with an MXFP4 key
+        store packed codes and scale bytes (select_bf16 as in lightning_indexer_topk_mxfp4)."""
         max_n = max(self.len_host) // M
         if workspace is None:
             workspace = torch.empty(max(csa_indexer_workspace_size(q_seq.numel(), max(max_n, 1), k), 256),
                                     dtype=torch.uint8, device=self.device)
+        if self.idx_fmt == CSA_IDX_MXFP4:
+            lightning_indexer_topk_mxfp4(qI, qs, w, self.kI, self.ks, self.seq_len, None, q_seq,
+                                         q_pos, idx_out, workspace, B=self.B, H_I=H_I,
+                                         d_I=self.d_I, m=M, k=k, max_n=max(max_n, 1),
+                                         select_bf16=select_bf16, layout=self.layout,
+                                         dev_status=self.dev_status, stream=stream)
+            return
         lightning_indexer_topk(qI, qs, w, self.kI, self.ks, self.seq_len, None, q_seq, q_pos,
                                idx_out, workspace, B=self.B, H_I=H_I, d_I=self.d_I, m=M, k=k,
                                max_n=max(max_n, 1), layout=self.layout,

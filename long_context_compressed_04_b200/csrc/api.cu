@@ -466,4 +466,191 @@ csa_status_t dense_hca_attn(const void* q, const void* entries, int32_t fmt, int
     return cuda_status(csa::launch_attn_simt(a, Q, D, (cudaStream_t)stream), "attention launch");
 }
 
+// ---- the indexer's inputs -----------------------------------------------------------------
+static int elem_bytes(int32_t dtype) { return dtype == CSA_DT_F32 ? 4 : 2; }
+
+#define REQUIRE_DTYPE(dtype)                                                               \
+    REQUIRE((dtype) == CSA_DT_BF16 || (dtype) == CSA_DT_F16 || (dtype) == CSA_DT_F32,      \
+            "unknown element type %d", (int)(dtype))
+#define REQUIRE_LAYOUT(l) \
+    REQUIRE((l) == CSA_SF_ROWS || (l) == CSA_SF_TILED, "unknown scale layout %d", (int)(l))
+
+size_t csa_mxfp4_sf_bytes(int64_t rows, int64_t cols, int32_t sf_layout) {
+    if (rows <= 0 || cols <= 0) return 0;
+    if (sf_layout == CSA_SF_TILED)
+        return (size_t)((rows + 127) / 128) * (size_t)((cols + 127) / 128) * 512;
+    return (size_t)rows * (size_t)(cols / 32);
+}
+
+// Sizes of an MXFP4 matrix (rows >= 0 checked here too, before the no-op return).
+static csa_status_t mxfp4_sizes(int64_t rows, int64_t cols) {
+    REQUIRE(rows >= 0, "row counts must be >= 0");
+    REQUIRE(cols >= 32 && cols % 32 == 0, "%lld columns: must be a positive multiple of 32",
+            (long long)cols);
+    SUPPORT(cols <= (1 << 20), "%lld columns not supported (up to 2^20)", (long long)cols);
+    SUPPORT(rows <= (1ll << 31) - 256 && rows <= (1ll << 40) / cols,
+            "%lld rows of %lld columns not supported", (long long)rows, (long long)cols);
+    return CSA_OK;
+}
+
+csa_status_t csa_mxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols,
+                                int64_t ld, uint8_t* codes, uint8_t* sf, int32_t sf_layout,
+                                int32_t* dev_status, void* stream) {
+    REQUIRE_DTYPE(dtype);
+    REQUIRE_LAYOUT(sf_layout);
+    csa_status_t v = mxfp4_sizes(rows, cols);
+    if (v != CSA_OK) return v;
+    if (rows == 0) return ok();
+    REQUIRE(x && codes && sf, "null pointer argument");
+    REQUIRE(aligned(x, 16) && aligned(codes, 16), "x and codes must be 16-byte aligned");
+    REQUIRE(ld >= cols && ld * elem_bytes(dtype) % 16 == 0,
+            "row stride %lld must be >= cols and a multiple of 16 bytes", (long long)ld);
+    return cuda_status(csa::launch_mxfp4_quantize(x, dtype, rows, cols, ld, codes, sf,
+                                                  sf_layout == CSA_SF_TILED, dev_status,
+                                                  (cudaStream_t)stream),
+                       "MXFP4 quantisation launch");
+}
+
+csa_status_t csa_mxfp4_dequantize(const uint8_t* codes, const uint8_t* sf, int32_t sf_layout,
+                                  int64_t rows, int64_t cols, void* out, int32_t dtype,
+                                  int64_t ld, void* stream) {
+    REQUIRE_DTYPE(dtype);
+    REQUIRE_LAYOUT(sf_layout);
+    csa_status_t v = mxfp4_sizes(rows, cols);
+    if (v != CSA_OK) return v;
+    if (rows == 0) return ok();
+    REQUIRE(codes && sf && out, "null pointer argument");
+    REQUIRE(aligned(out, 16) && aligned(codes, 16), "codes and out must be 16-byte aligned");
+    REQUIRE(ld >= cols && ld * elem_bytes(dtype) % 16 == 0,
+            "row stride %lld must be >= cols and a multiple of 16 bytes", (long long)ld);
+    return cuda_status(csa::launch_mxfp4_dequantize(codes, sf, sf_layout == CSA_SF_TILED, rows,
+                                                    cols, out, dtype, ld, (cudaStream_t)stream),
+                       "MXFP4 dequantisation launch");
+}
+
+csa_status_t csa_mxfp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b,
+                              const uint8_t* b_sf, int64_t M, int64_t N, int64_t K, void* out,
+                              int32_t dtype, int64_t ld, int32_t* dev_status, void* stream) {
+    REQUIRE_DTYPE(dtype);
+    csa_status_t v = mxfp4_sizes(M, K);
+    if (v == CSA_OK) v = mxfp4_sizes(N, K);
+    if (v != CSA_OK) return v;
+    if (M == 0 || N == 0) return ok();
+    REQUIRE(a && a_sf && b && b_sf && out, "null pointer argument");
+    REQUIRE(aligned(a, 16) && aligned(a_sf, 16) && aligned(b, 16) && aligned(b_sf, 16),
+            "a, a_sf, b and b_sf must be 16-byte aligned");
+    REQUIRE(aligned(out, elem_bytes(dtype)) && ld >= N, "bad out alignment or row stride");
+    SUPPORT(M <= (1 << 23), "M = %lld not supported (up to 2^23)", (long long)M);
+    return cuda_status(csa::launch_mxfp4_matmul(a, a_sf, b, b_sf, (int)M, (int)N, (int)K, out,
+                                                dtype, ld, dev_status, (cudaStream_t)stream),
+                       "MXFP4 product launch");
+}
+
+// Norm / rotation parameters shared by the three row calls; `step`: rope_dims' granularity.
+static csa_status_t rope_validate(int32_t D, int32_t rope, int step, int32_t norm, float theta,
+                                  float eps, const float* w0, const float* w1) {
+    REQUIRE(rope >= 0 && rope <= D && rope % step == 0,
+            "rope_dims %d must be a multiple of %d in 0..%d", rope, step, D);
+    SUPPORT(rope <= 2 * csa::kMaxRopePairs, "rope_dims %d not supported (up to %d)", rope,
+            2 * csa::kMaxRopePairs);
+    REQUIRE(norm == 0 || norm == 1, "norm must be 0 or 1");
+    REQUIRE(theta > 1.f && eps >= 0.f, "rope_theta must be > 1 and eps >= 0");
+    REQUIRE(aligned(w0, 16) && aligned(w1, 16), "weights must be 16-byte aligned");
+    return CSA_OK;
+}
+
+// [T, heads, D] rows: 16-byte aligned base and strides.
+static bool rows_aligned(const void* p, int64_t st, int64_t sh, int es) {
+    return aligned(p, 16) && st * es % 16 == 0 && sh * es % 16 == 0;
+}
+
+csa_status_t csa_qk_norm_rope(const void* q, int64_t q_st, int64_t q_sh, const void* k,
+                              int64_t k_st, int64_t k_sh, const int32_t* pos,
+                              const float* q_weight, const float* k_weight, void* q_out,
+                              int64_t qo_st, int64_t qo_sh, void* k_out, int64_t ko_st,
+                              int64_t ko_sh, int32_t dtype, int32_t T, int32_t H, int32_t Hk,
+                              int32_t D, int32_t rope_dims, int32_t norm, float rope_theta,
+                              float eps, void* stream) {
+    REQUIRE_DTYPE(dtype);
+    REQUIRE(T >= 0 && H >= 0 && Hk >= 0, "T, H and Hk must be >= 0");
+    SUPPORT(H <= (1 << 20) && Hk <= (1 << 20), "more than 2^20 heads not supported");
+    SUPPORT(D >= 8 && D <= 1024 && D % 8 == 0,
+            "head dim %d not supported (a multiple of 8 up to 1024)", D);
+    csa_status_t v = rope_validate(D, rope_dims, 2, norm, rope_theta, eps, q_weight, k_weight);
+    if (v != CSA_OK) return v;
+    if (T == 0 || H + Hk == 0) return ok();
+    REQUIRE(pos && (H == 0 || (q && q_out)) && (Hk == 0 || (k && k_out)), "null pointer argument");
+    const int es = elem_bytes(dtype);
+    REQUIRE((H == 0 || (rows_aligned(q, q_st, q_sh, es) && rows_aligned(q_out, qo_st, qo_sh, es))) &&
+                (Hk == 0 || (rows_aligned(k, k_st, k_sh, es) && rows_aligned(k_out, ko_st, ko_sh, es))),
+            "rows must be 16-byte aligned (pointers and strides)");
+    SUPPORT((int64_t)T * (H + Hk) <= (1ll << 32), "too many rows");
+    const csa::QkRows qr{q, q_out, q_weight, q_st, q_sh, qo_st, qo_sh, H};
+    const csa::QkRows kr{k, k_out, k_weight, k_st, k_sh, ko_st, ko_sh, Hk};
+    return cuda_status(csa::launch_qk_norm_rope(qr, kr, pos, dtype, T, D, rope_dims, norm,
+                                                rope_theta, eps, (cudaStream_t)stream),
+                       "norm and rotation launch");
+}
+
+// Stored format of the indexer's rows.
+static csa_status_t idx_validate(int32_t D, int32_t fmt, const uint8_t* codes, const void* scale) {
+    REQUIRE(fmt == CSA_IDX_FP8 || fmt == CSA_IDX_MXFP4, "unknown indexer format %d", fmt);
+    SUPPORT(D == 64 || D == 128, "indexer dim %d not supported (64 or 128)", D);
+    REQUIRE(aligned(codes, 16) && (fmt == CSA_IDX_MXFP4 || aligned(scale, 4)),
+            "codes must be 16-byte and fp32 scales 4-byte aligned");
+    return CSA_OK;
+}
+
+csa_status_t csa_indexer_queries(const void* q, int32_t dtype, int64_t q_st, int64_t q_sh,
+                                 const int32_t* q_pos, const float* weight, int32_t norm,
+                                 int32_t rope_dims, float rope_theta, float eps, int32_t Q,
+                                 int32_t H, int32_t D, int32_t fmt, uint8_t* codes, void* scale,
+                                 int32_t* dev_status, void* stream) {
+    REQUIRE_DTYPE(dtype);
+    REQUIRE(Q >= 0 && H >= 0, "Q and H must be >= 0");
+    SUPPORT(H <= (1 << 20), "more than 2^20 heads not supported");
+    csa_status_t v = idx_validate(D, fmt, codes, scale);
+    if (v == CSA_OK) v = rope_validate(D, rope_dims, 8, norm, rope_theta, eps, weight, nullptr);
+    if (v != CSA_OK) return v;
+    if (Q == 0 || H == 0) return ok();
+    REQUIRE(q && q_pos && codes && scale, "null pointer argument");
+    REQUIRE(rows_aligned(q, q_st, q_sh, elem_bytes(dtype)),
+            "query rows must be 16-byte aligned (pointer and strides)");
+    SUPPORT((int64_t)Q * H <= (1ll << 32), "too many rows");
+    return cuda_status(csa::launch_indexer_queries(q, dtype, q_st, q_sh, q_pos, weight, norm,
+                                                   rope_dims, rope_theta, eps, Q, H, D, fmt,
+                                                   codes, scale, dev_status, (cudaStream_t)stream),
+                       "indexer query launch");
+}
+
+csa_status_t csa_indexer_append(const void* k, int32_t dtype, int64_t k_ld,
+                                const int64_t* seq_len, const int64_t* ent_off,
+                                const int32_t* item_seq, const int32_t* item_ent, int64_t n_items,
+                                int32_t B, int32_t m, const float* weight, int32_t norm,
+                                int32_t rope_dims, float rope_theta, float eps, int32_t D,
+                                int32_t fmt, uint8_t* codes, void* scale, int64_t ent_rows,
+                                const csa_cache_layout_t* layout, int32_t* dev_status,
+                                void* stream) {
+    REQUIRE_DTYPE(dtype);
+    REQUIRE(n_items >= 0 && n_items < (1ll << 31), "n_items out of range: %lld", (long long)n_items);
+    csa_status_t v = idx_validate(D, fmt, codes, scale);
+    if (v == CSA_OK) v = rope_validate(D, rope_dims, 8, norm, rope_theta, eps, weight, nullptr);
+    if (v != CSA_OK) return v;
+    REQUIRE(B >= 1 && m >= 1, "B and m must be >= 1");
+    REQUIRE(ent_rows >= 0 && ent_rows < (1ll << 31), "ent_rows out of range");
+    if (n_items == 0) return ok();
+    REQUIRE(k && seq_len && item_seq && item_ent && codes && scale, "null pointer argument");
+    REQUIRE(aligned(k, 16) && k_ld >= D && k_ld * elem_bytes(dtype) % 16 == 0,
+            "keys must be 16-byte aligned (pointer and row stride), the stride >= D");
+    csa::EntryRows er;
+    csa::RawRows raw;
+    v = make_rows(layout, m, ent_off, nullptr, nullptr, false, &er, &raw);
+    if (v != CSA_OK) return v;
+    return cuda_status(csa::launch_indexer_append(k, dtype, k_ld, seq_len, er, item_seq, item_ent,
+                                                  n_items, ent_rows, B, m, weight, norm, rope_dims,
+                                                  rope_theta, eps, D, fmt, codes, scale,
+                                                  dev_status, (cudaStream_t)stream),
+                       "indexer key append launch");
+}
+
 }  // extern "C"

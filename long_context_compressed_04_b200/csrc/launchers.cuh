@@ -59,6 +59,12 @@ enum KernelKind {
     kKCpPackRows,
     kKIndexerFp4,
     kKCacheAppend,
+    kKMxQuant,
+    kKMxDequant,
+    kKMxMatmul,
+    kKQkNormRope,
+    kKIndexerQueries,
+    kKIndexerAppend,
     kKernelKinds
 };
 
@@ -146,6 +152,43 @@ cudaError_t launch_cache_append(const uint16_t* kv_new, const uint16_t* gate_new
                                 int m, int64_t kv_rows, int64_t ent_rows, uint16_t* kv,
                                 uint16_t* gate, uint8_t* kI, float* ks, int32_t* st,
                                 cudaStream_t stream);
+
+cudaError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld,
+                                  uint8_t* codes, uint8_t* sf, int tiled, int32_t* st,
+                                  cudaStream_t stream);
+cudaError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* sf, int tiled,
+                                    int64_t rows, int64_t cols, void* out, int dtype, int64_t ld,
+                                    cudaStream_t stream);
+cudaError_t launch_mxfp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b,
+                                const uint8_t* b_sf, int M, int N, int K, void* out, int dtype,
+                                int64_t ld, int32_t* st, cudaStream_t stream);
+
+// Frequencies theta^(-2j / rope) of the rotation pairs (at most 128 rotated channels).
+constexpr int kMaxRopePairs = 64;
+struct RopeTable {
+    double freq[kMaxRopePairs];
+};
+// Head rows of a qk_norm_rope call: element strides between tokens (st) and heads (sh).
+struct QkRows {
+    const void* x;
+    void* out;
+    const float* weight;
+    int64_t st, sh, ost, osh;
+    int heads;
+};
+cudaError_t launch_qk_norm_rope(const QkRows& q, const QkRows& k, const int32_t* pos, int dtype, int T,
+                                int D, int rope, int norm, float theta, float eps,
+                                cudaStream_t stream);
+cudaError_t launch_indexer_queries(const void* q, int dtype, int64_t st, int64_t sh, const int32_t* pos,
+                                   const float* weight, int norm, int rope, float theta, float eps,
+                                   int Q, int H, int D, int fmt, uint8_t* codes, void* scale,
+                                   int32_t* dev_status, cudaStream_t stream);
+cudaError_t launch_indexer_append(const void* k, int dtype, int64_t ld, const int64_t* seq_len,
+                                  const EntryRows& er, const int32_t* item_seq,
+                                  const int32_t* item_ent, int64_t n, int64_t ent_rows, int B, int m,
+                                  const float* weight, int norm, int rope, float theta, float eps,
+                                  int D, int fmt, uint8_t* codes, void* scale, int32_t* dev_status,
+                                  cudaStream_t stream);
 
 // Sets the thread-local message csa_last_error() returns (printf-style).
 void set_error_message(const char* fmt, ...);

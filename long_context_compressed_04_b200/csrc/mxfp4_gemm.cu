@@ -1,0 +1,289 @@
+// MXFP4 product on the 5th-generation tensor cores: out[m, n] = sum_k A[m, k] B[n, k]
+// ("DeepSeek-V4 深度分析报告" 3.4: MXFP4 weights and activations; batch-invariant GEMMs without
+// split-K, 3.3).
+//
+// B's rows (the weight's output features) lie on the 128 lanes of the accumulator and A's
+// rows (tokens) on its columns, whatever the batch: a decode step of a few tokens then
+// still streams the weight 128 (or RT) rows at a time, and a result's products are summed in the
+// same order, K ascending, by the same instruction at every batch size.
+//
+//   warp 0 lane 0  TMA producer: per stage of K = 256 the RT weight rows and NT token rows
+//                  (128 bytes each, 128-byte swizzle) and their scale tiles (bulk copies:
+//                  the tiled scale layout is the tensor cores' own);
+//   warp 1         TMEM allocation; lane 0 copies the scales into TMEM (one slot of columns
+//                  per stage: a slot is refilled only after the MMAs that read it) and
+//                  issues tcgen05.mma kind::mxf4.block_scale, K = 64 an instruction;
+//   warps 2-5      epilogue: a thread holds one output feature and walks the tokens; the 32
+//                  lanes of a warp write consecutive features.
+//
+// Every wait is bounded; a timeout aborts the CTA, drains its copies and MMAs, frees TMEM and
+// reports CSA_DEV_TIMEOUT.
+#include "launchers.cuh"
+#include "rows.cuh"
+#include "sm100.cuh"
+
+namespace csa {
+
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kStageK = 256;             // elements of K per stage: 128 bytes a row
+constexpr int kRowB = kStageK / 2;
+constexpr int kWTile = 128 * kRowB;      // a stage's weight rows (the MMA reads 128)
+constexpr int kSfTile = 512;             // scales of 128 rows x 4 blocks
+
+template <int NT>
+constexpr int token_tiles() { return NT > 128 ? 2 : 1; }   // 128-row scale tiles
+template <int NT>
+constexpr int stage_bytes() { return kWTile + NT * kRowB + 2 * kSfTile * (1 + token_tiles<NT>()); }
+template <int NT>
+constexpr int stages() {
+    const int s = (220 * 1024) / stage_bytes<NT>();
+    return s > 10 ? 10 : s;
+}
+// TMEM columns: NT of accumulator, then per stage 8 of weight scales and 8 per token tile.
+template <int NT>
+constexpr int sf_cols() { return 8 * (1 + token_tiles<NT>()); }
+template <int NT>
+constexpr uint32_t tmem_cols() {
+    const int c = NT + stages<NT>() * sf_cols<NT>();
+    return c <= 128 ? 128u : c <= 256 ? 256u : 512u;
+}
+
+struct GemmArgs {
+    const uint8_t* a_sf;
+    const uint8_t* b_sf;
+    void* out;
+    int64_t ld;
+    int32_t* st;
+    int M, N, K, dtype;
+    int kt128;        // scale tiles along K
+};
+
+__device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float v) {
+    if (dtype == CSA_DT_BF16) reinterpret_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+    else if (dtype == CSA_DT_F16) reinterpret_cast<__half*>(out)[i] = __float2half_rn(v);
+    else reinterpret_cast<float*>(out)[i] = v;
+}
+
+// grid (weight row tiles of RT, token tiles of NT)
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b,
+                      const __grid_constant__ CUtensorMap tmap_a, const GemmArgs g, const int RT) {
+    using namespace sm100;
+    constexpr int S = stages<NT>(), kTT = token_tiles<NT>();
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    uint8_t* sW = smem;                                  // [S][128 rows x 128 B]
+    uint8_t* sX = sW + S * kWTile;                       // [S][NT rows x 128 B]
+    uint8_t* sSw = sX + S * NT * kRowB;                  // [S][2][512]
+    uint8_t* sSx = sSw + S * 2 * kSfTile;                // [S][kTT][2][512]
+    uint64_t* full = reinterpret_cast<uint64_t*>(sSx + S * kTT * 2 * kSfTile);
+    uint64_t* empty = full + S;
+    uint64_t* accfull = empty + S;
+    uint64_t* drain = accfull + 1;
+    uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_smem + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n0 = blockIdx.x * RT, m0 = blockIdx.y * NT;
+    const int row0 = n0 & 127;                // the tile's first lane: its place in its scale tile
+    const int nk = (g.K + kStageK - 1) / kStageK;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; s++) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(accfull, 1);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+        prefetch_tmap(&tmap_b);
+        prefetch_tmap(&tmap_a);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_base_smem, tmem_cols<NT>());
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_base_smem;
+    pdl_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint8_t* bsf = g.b_sf + (int64_t)(n0 >> 7) * g.kt128 * kSfTile;
+            int n_load = 0;
+            for (int i = 0; i < nk; i++) {
+                const int s = i % S;
+                if (!mbar_wait(&empty[s], ((i / S) & 1) ^ 1, abort_flag, g.st)) break;
+                const uint32_t sfb = (uint32_t)min(2, g.kt128 - 2 * i) * kSfTile;
+                int tt = 0;       // token scale tiles that exist
+                for (int t = 0; t < kTT; t++) tt += m0 + 128 * t < g.M ? 1 : 0;
+                mbar_arrive_expect_tx(&full[s], RT * kRowB + NT * kRowB + sfb * (1 + tt));
+                tma_load_2d(sW + s * kWTile + row0 * kRowB, &tmap_b, &full[s], i * kRowB, n0);
+                tma_load_2d(sX + s * NT * kRowB, &tmap_a, &full[s], i * kRowB, m0);
+                bulk_load(sSw + s * 2 * kSfTile, bsf + (int64_t)2 * i * kSfTile, sfb, &full[s]);
+                for (int t = 0; t < tt; t++)
+                    bulk_load(sSx + (s * kTT + t) * 2 * kSfTile,
+                              g.a_sf + ((int64_t)((m0 >> 7) + t) * g.kt128 + 2 * i) * kSfTile, sfb,
+                              &full[s]);
+                n_load++;
+            }
+            for (int s = 0; s < S; s++) {
+                const int cnt = n_load / S + (s < n_load % S ? 1 : 0);
+                if (cnt) mbar_drain(&full[s], (cnt - 1) & 1, g.st);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            bool ok = true;
+            for (int i = 0; i < nk; i++) {
+                const int s = i % S;
+                if (!mbar_wait(&full[s], (i / S) & 1, abort_flag, g.st)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int kleft = g.K - i * kStageK;
+                const uint32_t sfw = tmem + (uint32_t)(NT + s * sf_cols<NT>()), sfx = sfw + 8;
+#pragma unroll
+                for (int kt = 0; kt < 2; kt++)
+                    if (128 * kt < kleft) {
+                        tmem_cp_32x128b_x4(sfw + 4 * kt, smem_desc_rows16(sSw + (s * 2 + kt) * kSfTile));
+#pragma unroll
+                        for (int t = 0; t < kTT; t++)
+                            tmem_cp_32x128b_x4(sfx + 4 * (kt * kTT + t),
+                                               smem_desc_rows16(sSx + ((s * kTT + t) * 2 + kt) * kSfTile));
+                    }
+                const uint64_t wd = smem_desc_k_sw128(sW + s * kWTile);
+                const uint64_t xd = smem_desc_k_sw128(sX + s * NT * kRowB);
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    if (64 * j < kleft) {
+                        const uint32_t id = 2 * (j & 1), sel = id << 30;
+                        mma_mxf4(tmem, wd + 2 * j, xd + 2 * j, instr_desc_mxf4(128, NT, id, id),
+                                 (sfw + 4 * (j >> 1)) | sel, (sfx + 4 * kTT * (j >> 1)) | sel,
+                                 i > 0 || j > 0 ? 1u : 0u);
+                    }
+                mma_commit(&empty[s]);
+            }
+            if (ok) mma_commit(accfull);
+            mma_commit(drain);
+            mbar_drain(drain, 0, g.st);
+        }
+    } else {
+        const int quarter = warp & 3;
+        const int r = quarter * 32 + lane;       // accumulator lane
+        const int n = n0 - row0 + r;
+        if (mbar_wait_warp(accfull, 0, abort_flag, g.st)) {
+            tc_fence_after();
+            const bool in = r >= row0 && r < row0 + RT && n < g.N;
+            const int tokens = min(NT, g.M - m0);
+            const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16);
+            for (int c = 0; c < tokens; c += 16) {
+                uint32_t d[16];
+                tmem_ld16(taddr + (uint32_t)c, d);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; j++)
+                    if (in && c + j < tokens)
+                        store_out(g.out, g.dtype, (int64_t)(m0 + c + j) * g.ld + n, __uint_as_float(d[j]));
+            }
+            tc_fence_before();
+        }
+        __threadfence();   // visible before the next kernel's reads ahead of its own wait
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, tmem_cols<NT>());
+    }
+}
+
+template <int NT>
+size_t smem_bytes() {
+    return 1024 + (size_t)stages<NT>() * stage_bytes<NT>() + (2 * stages<NT>() + 2) * 8 + 16;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+// Row-major [rows x row_bytes] byte matrix, boxes of box_rows x 128 bytes, 128-byte swizzle;
+// bytes past a row or the last row read as zeros.
+bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows) {
+    EncodeFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {row_bytes, rows};
+    const cuuint64_t strides[1] = {row_bytes};
+    const cuuint32_t box[2] = {(cuuint32_t)kRowB, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+template <int NT>
+cudaError_t run(const uint8_t* a, const uint8_t* b, const GemmArgs& g, int RT, cudaStream_t stream) {
+    CUtensorMap mb, ma;
+    if (!make_map(&mb, b, (uint64_t)g.N, (uint64_t)g.K / 2, (uint32_t)RT) ||
+        !make_map(&ma, a, (uint64_t)g.M, (uint64_t)g.K / 2, (uint32_t)NT))
+        return cudaErrorInvalidValue;
+    const size_t sm = smem_bytes<NT>();
+    cudaError_t e = cudaFuncSetAttribute(mxfp4_gemm_kernel<NT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+    if (e != cudaSuccess) return e;
+    LaunchScope scope(kKMxMatmul, stream);
+    return launch_pdl(mxfp4_gemm_kernel<NT>, dim3((g.N + RT - 1) / RT, (g.M + NT - 1) / NT),
+                      dim3(kThreads), sm, stream, mb, ma, g, RT);
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess)
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n > 0 ? n : 148;
+}
+
+}  // namespace
+
+cudaError_t launch_mxfp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b,
+                                const uint8_t* b_sf, int M, int N, int K, void* out, int dtype,
+                                int64_t ld, int32_t* st, cudaStream_t stream) {
+    const GemmArgs g{a_sf, b_sf, out, ld, st, M, N, K, dtype, (K + 127) / 128};
+    const int sms = sm_count();
+    const int NT = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+    // weight rows a CTA takes: 128, or fewer while the tiles leave SMs without one
+    int RT = 128;
+    const int mt = (M + NT - 1) / NT;
+    while (RT > 32 && (int64_t)((N + RT / 2 - 1) / (RT / 2)) * mt <= sms) RT /= 2;
+    switch (NT) {
+        case 16: return run<16>(a, b, g, RT, stream);
+        case 32: return run<32>(a, b, g, RT, stream);
+        case 64: return run<64>(a, b, g, RT, stream);
+        case 128: return run<128>(a, b, g, RT, stream);
+        default: return run<256>(a, b, g, RT, stream);
+    }
+}
+
+}  // namespace csa

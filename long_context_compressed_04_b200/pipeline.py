@@ -10,8 +10,9 @@ from typing import Optional
 
 import torch
 
-from . import (CSA_KV_BF16, csa_compress, csa_entry_row_bytes, csa_indexer_workspace_size,
-               dense_hca_attn, dense_hca_workspace_size, hca_compress, lightning_indexer_topk,
+from . import (CSA_IDX_FP8, CSA_KV_BF16, CSA_SF_TILED, csa_compress, csa_entry_row_bytes,
+               csa_indexer_queries, csa_indexer_workspace_size, csa_mxfp4_matmul,
+               csa_mxfp4_quantize, csa_mxfp4_sf_bytes, dense_hca_attn, dense_hca_workspace_size, hca_compress, lightning_indexer_topk,
                lightning_indexer_topk_mxfp4, sparse_mqa_attn)
 from .synth import Workload
 
@@ -115,3 +116,48 @@ def step(wl: Workload, buf: Buffers, item_seq, item_ent, stream=None):
     elif wl.H_I:
         indexer_topk(wl, buf, stream=stream)
     attend(wl, buf, stream)
+
+
+class QueryProjection:
+    """The indexer's query heads from hidden states: an MXFP4 projection, then the heads'
+    norm, rotation and quantisation (csa_mxfp4_quantize, csa_mxfp4_matmul,
+    csa_indexer_queries).  The weight is quantised once; the buffers of up to ``max_q``
+    query tokens are allocated here, so calls allocate nothing and can be captured.  Calls
+    share them: order calls of one projection on one stream."""
+
+    def __init__(self, weight: torch.Tensor, H_I: int, d_I: int, max_q: int,
+                 fmt: int = CSA_IDX_FP8, head_weight: Optional[torch.Tensor] = None,
+                 theta: float = 10000.0, eps: float = 1e-6):
+        N, K = weight.shape
+        if N != H_I * d_I:
+            raise ValueError(f"weight has {N} rows, not H_I * d_I = {H_I * d_I}")
+        dev = weight.device
+        u8 = lambda *n: torch.empty(n, dtype=torch.uint8, device=dev)  # noqa: E731
+        self.H_I, self.d_I, self.K, self.fmt, self.max_q = H_I, d_I, K, fmt, max_q
+        self.head_weight, self.theta, self.eps = head_weight, theta, eps
+        self.w, self.w_sf = u8(N, K // 2), u8(csa_mxfp4_sf_bytes(N, K, CSA_SF_TILED))
+        csa_mxfp4_quantize(weight, self.w, self.w_sf, sf_layout=CSA_SF_TILED)
+        self.x, self.x_sf = u8(max_q, K // 2), u8(csa_mxfp4_sf_bytes(max_q, K, CSA_SF_TILED))
+        self.heads = torch.empty((max_q, H_I, d_I), dtype=torch.bfloat16, device=dev)
+        if fmt == CSA_IDX_FP8:
+            self.codes = u8(max_q, H_I, d_I)
+            self.scale = torch.empty((max_q, H_I), dtype=torch.float32, device=dev)
+        else:
+            self.codes, self.scale = u8(max_q, H_I, d_I // 2), u8(max_q, H_I, d_I // 32)
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def __call__(self, x: torch.Tensor, q_pos: torch.Tensor, stream=None):
+        """x [Q, K] (bf16, fp16 or fp32), q_pos int32 [Q]: the query heads' codes and scales,
+        views of this projection's buffers that the next call overwrites."""
+        Q = x.shape[0]
+        if Q > self.max_q or x.shape[1] != self.K:
+            raise ValueError(f"x is {tuple(x.shape)}: at most {self.max_q} rows of {self.K}")
+        heads, codes, scale = self.heads[:Q], self.codes[:Q], self.scale[:Q]
+        csa_mxfp4_quantize(x, self.x[:Q], self.x_sf, sf_layout=CSA_SF_TILED,
+                           dev_status=self.dev_status, stream=stream)
+        csa_mxfp4_matmul(self.x[:Q], self.x_sf, self.w, self.w_sf, heads.flatten(1),
+                         dev_status=self.dev_status, stream=stream)
+        csa_indexer_queries(heads, q_pos, codes, scale, fmt=self.fmt, weight=self.head_weight,
+                            rope_theta=self.theta, eps=self.eps, dev_status=self.dev_status,
+                            stream=stream)
+        return codes, scale

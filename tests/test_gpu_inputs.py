@@ -1,0 +1,403 @@
+"""GPU parity of the operators that make the indexer's inputs with their 64-bit forms.
+
+Codes, scale bytes, stored query heads and keys are compared bit for bit: the quantisers
+are exact by construction.  Products of inputs whose sums fp32 holds exactly have to equal the
+rounded 64-bit product; others are held to a bound from the accumulation order.  Norm and
+rotation in fp32 are held to a bound counted in roundings."""
+import numpy as np
+import pytest
+import torch
+
+import _inputs_orc as io
+import long_context_compressed_04_b200 as L
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+def _status():
+    return torch.zeros(1, dtype=torch.int32, device=DEV)
+
+
+def _sync(st, want=0):
+    torch.cuda.synchronize()
+    assert int(st.item()) == want
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _gpu(a, dtype=None):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV) if dtype is None else \
+        torch.from_numpy(np.ascontiguousarray(a)).to(DEV).to(dtype)
+
+
+def _sf_empty(rows, cols, lay):
+    n = L.csa_mxfp4_sf_bytes(rows, cols, lay)
+    return torch.full((n,) if lay == L.CSA_SF_TILED else (rows, cols // 32), 0xAA, dtype=torch.uint8,
+                      device=DEV)
+
+
+# ---- MXFP4 quantisation --------------------------------------------------------------------
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("tiled", [False, True])
+@pytest.mark.parametrize("rows,cols,pad", [(1, 32, 0), (3, 96, 8), (127, 160, 0), (129, 128, 32),
+                                           (1000, 2048, 0), (33, 4064, 16)])
+def test_quantize_and_back_bit_exact(rows, cols, pad, tiled, dt):
+    g = torch.Generator(device=DEV).manual_seed(rows + cols)
+    x = torch.randn((rows, cols + pad), generator=g, device=DEV)
+    x *= torch.exp2(torch.randint(-8, 9, (rows, 1), generator=g, device=DEV).float())
+    x = x.to(DT[dt])[:, :cols]
+    lay = L.CSA_SF_TILED if tiled else L.CSA_SF_ROWS
+    codes = torch.full((rows, cols // 2), 0x55, dtype=torch.uint8, device=DEV)
+    sf, st = _sf_empty(rows, cols, lay), _status()
+    L.csa_mxfp4_quantize(x, codes, sf, sf_layout=lay, dev_status=st)
+    _sync(st)
+    p, s = io.mxfp4(f64(x))
+    assert np.array_equal(codes.cpu().numpy(), p)
+    assert np.array_equal(sf.cpu().numpy(), io.tile_scales(s) if tiled else s)
+    ref = io.mxfp4_values(p, s)
+    for out_dt in DT.values():
+        out = torch.full((rows, cols + pad), 7.0, dtype=out_dt, device=DEV)
+        L.csa_mxfp4_dequantize(codes, sf, out[:, :cols], sf_layout=lay)
+        torch.cuda.synchronize()
+        want = torch.from_numpy(ref).to(out_dt)
+        assert torch.equal(out[:, :cols].cpu(), want)
+        assert bool((out[:, cols:] == 7.0).all())
+
+
+def test_quantize_borders_and_extremes():
+    # every midpoint (a tie) and its neighbours in fp32, at scales over the whole exponent
+    # range (subnormals among them), zeros of both signs
+    mids = (io.LEVELS[1:] + io.LEVELS[:-1]) / 2
+    base = np.concatenate([mids, mids * (1 + 2.0 ** -22), mids * (1 - 2.0 ** -22), io.LEVELS[1:]])
+    base = np.concatenate([base, [0.0, -0.0, 6.0, 4.0]])
+    rows = [np.roll(base, r) * (-1) ** np.arange(32) * 2.0 ** e
+            for r, e in enumerate([0, 1, -1, 60, -60, 125, -126, -128, -133, -149])]
+    rows += [np.zeros(32), -np.zeros(32), np.full(32, 2.0 ** -149),
+             np.full(32, np.finfo(np.float32).max)]
+    x = np.stack(rows).astype(np.float32)
+    codes = torch.empty((len(x), 16), dtype=torch.uint8, device=DEV)
+    sf, st = _sf_empty(len(x), 32, 0), _status()
+    L.csa_mxfp4_quantize(_gpu(x), codes, sf, dev_status=st)
+    _sync(st)
+    p, s = io.mxfp4(x.astype(np.float64))
+    assert np.array_equal(sf.cpu().numpy(), s)
+    assert np.array_equal(codes.cpu().numpy(), p)
+    out = torch.empty((len(x), 32), device=DEV)
+    L.csa_mxfp4_dequantize(codes, sf, out)
+    torch.cuda.synchronize()
+    assert np.array_equal(f64(out), io.mxfp4_values(p, s).astype(np.float32).astype(np.float64))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_quantize_marks_non_finite_blocks(bad):
+    x = torch.randn((40, 128), device=DEV).to(torch.bfloat16)
+    x[17, 70] = bad
+    codes, sf, st = torch.empty((40, 64), dtype=torch.uint8, device=DEV), _sf_empty(40, 128, 0), _status()
+    L.csa_mxfp4_quantize(x, codes, sf, dev_status=st)
+    _sync(st, L.CSA_DEV_NAN)
+    p, s = io.mxfp4(f64(x))
+    assert s[17, 2] == 255 and (s == 255).sum() == 1
+    assert np.array_equal(codes.cpu().numpy(), p) and np.array_equal(sf.cpu().numpy(), s)
+    out = torch.empty((40, 128), device=DEV)
+    L.csa_mxfp4_dequantize(codes, sf, out)
+    assert bool(out[17, 64:96].isnan().all()) and int(out.isnan().sum()) == 32
+
+
+# ---- MXFP4 product ---------------------------------------------------------------------------
+def _operands(rng, M, N, K, lo, hi):
+    """Random codes and scale bytes, and their values."""
+    out = []
+    for r in (M, N):
+        c = rng.integers(0, 16, (r, K)).astype(np.uint8)
+        s = rng.integers(lo, hi + 1, (r, K // 32)).astype(np.uint8)
+        out.append((io.pack(c), s, io.mxfp4_values(io.pack(c), s)))
+    return out
+
+
+def _matmul(a, b, dt, ld=None, st=None, fill=0):
+    M, N = len(a[0]), len(b[0])
+    out = torch.full((M, ld or N), 3.0, dtype=DT[dt], device=DEV)
+    L.csa_mxfp4_matmul(_gpu(a[0]), _gpu(io.tile_scales(a[1], fill)), _gpu(b[0]),
+                       _gpu(io.tile_scales(b[1], fill)), out[:, :N], dev_status=st)
+    return out
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 32), (1, 128, 64), (3, 130, 96), (8, 8192, 256),
+                                   (16, 96, 2048), (17, 333, 544), (33, 64, 1504), (65, 4104, 288),
+                                   (128, 200, 1024), (129, 77, 160), (300, 515, 2048),
+                                   (1000, 1111, 320), (513, 20000, 64)])
+def test_matmul_exact_sums_bit_exact(M, N, K, dt):
+    # block exponents -1 .. 0: every partial sum is a multiple of 1/16 below 2^20 (36 * K),
+    # so fp32 holds it whatever the order; the one rounding left is that to the output type
+    rng = np.random.default_rng(M * 7 + N + K)
+    a, b = _operands(rng, M, N, K, 126, 127)
+    st = _status()
+    out = _matmul(a, b, dt, ld=N + 5, st=st)
+    _sync(st)
+    want = torch.from_numpy(a[2] @ b[2].T).to(DT[dt])
+    got = out[:, :N].cpu()
+    assert torch.equal(got, want), (got.float() - want.float()).abs().max()
+    assert bool((out[:, N:] == 3.0).all())
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 300, 4096), (200, 256, 1504), (40, 130, 32)])
+def test_matmul_wide_scales(M, N, K):
+    # block exponents spread over 2^-12 .. 2^12: sums round.  Accumulating K / 64 instructions'
+    # sums of 64 products, each addition off by at most 2^-22 of the sum of magnitudes (a
+    # truncated alignment among the products of an instruction included): (K / 64 + 2) 2^-22
+    rng = np.random.default_rng(K)
+    a, b = _operands(rng, M, N, K, 115, 139)
+    out = _matmul(a, b, "f32")
+    torch.cuda.synchronize()
+    err = np.abs(f64(out) - a[2] @ b[2].T)
+    bound = (K / 64 + 2) * 2.0 ** -22 * (np.abs(a[2]) @ np.abs(b[2]).T) + 1e-300
+    assert np.all(err <= bound), (err / bound).max()
+
+
+def test_matmul_rows_do_not_depend_on_the_batch():
+    # the same rows at every batch size (every token tile width), wide scales so that the
+    # order of the additions shows in the last bits
+    rng = np.random.default_rng(5)
+    a, b = _operands(rng, 700, 260, 1536, 115, 139)
+    full = _matmul(a, b, "f32")
+    for lo, n in [(0, 1), (3, 5), (100, 16), (40, 31), (10, 64), (200, 127), (300, 200), (444, 256)]:
+        part = _matmul([x[lo:lo + n] for x in a], b, "f32")
+        assert torch.equal(part.view(torch.int32), full[lo:lo + n].view(torch.int32)), (lo, n)
+    # ... nor on the weight's other rows
+    for lo, n in [(0, 100), (128, 32), (224, 36)]:
+        part = _matmul(a, [x[lo:lo + n] for x in b], "f32")
+        assert torch.equal(part.view(torch.int32), full[:, lo:lo + n].contiguous().view(torch.int32))
+
+
+def test_matmul_nan_scales_reach_their_results_only():
+    rng = np.random.default_rng(6)
+    M, N, K = 20, 140, 160
+    a, b = _operands(rng, M, N, K, 126, 127)
+    a[1][7, 4], b[1][131, 0] = 255, 255
+    out = f64(_matmul(a, b, "f32"))
+    want = a[2] @ b[2].T
+    want[7, :] = np.nan
+    want[:, 131] = np.nan
+    assert np.array_equal(np.isnan(out), np.isnan(want))
+    ok = ~np.isnan(want)
+    assert np.array_equal(out[ok], want[ok])
+
+
+# ---- norm and rotation ---------------------------------------------------------------------
+def _qk_bound(x, w, rope, D, y, dt):
+    """Of fp32 roundings of 2^-24: the sum of squares takes 8 ceil(D / 256) + 5 additions per
+    lane chain and their halves reach y, rsqrtf 2 ulp (4), the division and eps sum 2, the
+    product with the weight and with x 2, cos and sin 2 (the reduced angle and sincos), the
+    rotation's products and sum 3; relative to |u| + |v| in rotated channels.  Plus half a
+    step of the stored type."""
+    n = (8 * -(-D // 256) + 6) / 2 + 13
+    mag = np.abs(io.norm_rope(x, 0, w, rope=0))
+    if rope:
+        r = mag[..., D - rope:]
+        pair = r[..., 0::2] + r[..., 1::2]
+        mag[..., D - rope:] = np.repeat(pair, 2, -1)
+    fi = torch.finfo(DT[dt])
+    return n * 2.0 ** -24 * mag + np.abs(y) * fi.eps / 2 * (1 + 1e-3) + fi.tiny * fi.eps
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,H,Hk,D,rope", [(1, 1, 0, 8, 8), (1, 64, 1, 128, 64), (3, 5, 2, 64, 64),
+                                           (7, 128, 1, 576, 64), (50, 3, 3, 40, 22), (2, 16, 1, 128, 128),
+                                           (33, 4, 0, 264, 32), (5, 2, 1, 520, 0), (4, 7, 1, 1024, 128),
+                                           (300, 16, 1, 128, 64), (2000, 9, 1, 72, 64)])
+def test_qk_norm_rope(T, H, Hk, D, rope, dt):
+    g = torch.Generator(device=DEV).manual_seed(T + D)
+    q = torch.randn((T, H, D), generator=g, device=DEV) * torch.rand((T, H, 1), generator=g, device=DEV) * 4
+    k = torch.randn((T, Hk, D), generator=g, device=DEV) if Hk else None
+    q, k = q.to(DT[dt]), None if k is None else k.to(DT[dt])
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device=DEV, dtype=torch.int32)
+    qw = 1 + 0.2 * torch.randn(D, generator=g, device=DEV)
+    kw = None if Hk == 2 else 1 + 0.2 * torch.randn(D, generator=g, device=DEV)
+    qo, ko = torch.zeros_like(q), None if k is None else torch.zeros_like(k)
+    L.csa_qk_norm_rope(q, k, pos, qo, ko, q_weight=qw, k_weight=kw, rope_dims=rope)
+    torch.cuda.synchronize()
+    for x, o, w in ((q, qo, qw), (k, ko, kw)):
+        if x is None:
+            continue
+        w = None if w is None else f64(w)
+        y = io.norm_rope(f64(x), pos.cpu().numpy(), w, rope=rope)
+        err = np.abs(f64(o) - y)
+        bound = _qk_bound(f64(x), w, rope, D, y, dt)
+        assert np.all(err <= bound), (err / bound).max()
+
+
+def test_qk_norm_rope_strides_in_place_and_one_side():
+    g = torch.Generator(device=DEV).manual_seed(3)
+    T, H, D = 37, 6, 128
+    # one projection output [T, (H + 1) * D + 64]: q and k are slices of its rows
+    x = torch.randn((T, (H + 1) * D + 64), generator=g, device=DEV).to(torch.bfloat16)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV) * 1000
+    q, k = x[:, :H * D].unflatten(1, (H, D)), x[:, H * D:(H + 1) * D].unflatten(1, (1, D))
+    qo, ko = torch.empty((T, H, D), dtype=x.dtype, device=DEV), torch.empty((T, 1, D), dtype=x.dtype, device=DEV)
+    L.csa_qk_norm_rope(q, k, pos, qo, ko)
+    # head-major storage of both sides
+    qt = q.transpose(0, 1).contiguous().transpose(0, 1)
+    qto = torch.empty((H, T, D), dtype=x.dtype, device=DEV).transpose(0, 1)
+    L.csa_qk_norm_rope(qt, None, pos, qto, None)
+    kto = torch.empty_like(ko)
+    L.csa_qk_norm_rope(None, k, pos, None, kto)
+    tail = x[:, (H + 1) * D:].clone()
+    L.csa_qk_norm_rope(q, k, pos, q, k)           # in place
+    torch.cuda.synchronize()
+    assert torch.equal(q, qo) and torch.equal(k, ko) and torch.equal(qto, qo) and torch.equal(kto, ko)
+    assert torch.equal(x[:, (H + 1) * D:], tail)
+
+
+def test_qk_norm_rope_zero_rows_and_non_finite():
+    x = torch.randn((4, 3, 128), device=DEV)
+    x[1, 2] = 0
+    x[2, 0, 5] = float("nan")
+    pos = torch.full((4,), 9, dtype=torch.int32, device=DEV)
+    y = torch.empty_like(x)
+    L.csa_qk_norm_rope(x, None, pos, y, None)
+    torch.cuda.synchronize()
+    assert bool((y[1, 2] == 0).all())
+    assert bool(y[2, 0].isnan().all()) and int(y.isnan().sum()) == 128
+    # without the norm and the rotation the rows pass through
+    L.csa_qk_norm_rope(x, None, pos, y, None, norm=False, rope_dims=0)
+    torch.cuda.synchronize()
+    assert torch.equal(torch.nan_to_num(y, 5.0), torch.nan_to_num(x, 5.0))
+
+
+# ---- the indexer's query heads and keys ---------------------------------------------------------
+def _store(fmt, lead, D):
+    if fmt == L.CSA_IDX_FP8:
+        return (torch.full((*lead, D), 0x11, dtype=torch.uint8, device=DEV),
+                torch.full(lead, 0.5, device=DEV))
+    return (torch.full((*lead, D // 2), 0x11, dtype=torch.uint8, device=DEV),
+            torch.full((*lead, D // 32), 100, dtype=torch.uint8, device=DEV))
+
+
+def _quant_ref(y, fmt):
+    return io.fp8(y) if fmt == L.CSA_IDX_FP8 else io.mxfp4(y)
+
+
+def _same(codes, scale, ref):
+    assert np.array_equal(codes.cpu().numpy(), ref[0])
+    assert np.array_equal(scale.cpu().numpy(), ref[1], equal_nan=scale.dtype == torch.float32)
+
+
+@pytest.mark.parametrize("fmt", [L.CSA_IDX_FP8, L.CSA_IDX_MXFP4])
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("Q,H,D,norm,rope,weight", [(1, 1, 64, True, 64, False), (1, 64, 128, True, 64, True),
+                                                    (5, 4, 64, True, 32, True), (33, 16, 128, True, 128, False),
+                                                    (3, 7, 128, False, 0, False), (9, 5, 128, False, 64, True),
+                                                    (700, 32, 128, True, 64, True)])
+def test_indexer_queries_bit_exact(Q, H, D, norm, rope, weight, dt, fmt):
+    g = torch.Generator(device=DEV).manual_seed(Q * H + D)
+    x = torch.randn((Q, H, D + 32), generator=g, device=DEV)
+    x = (x * torch.exp2(torch.randint(-6, 7, (Q, H, 1), generator=g, device=DEV).float())).to(DT[dt])[..., :D]
+    pos = torch.randint(0, 1 << 20, (Q,), generator=g, device=DEV, dtype=torch.int32)
+    w = 1 + 0.2 * torch.randn(D, generator=g, device=DEV) if weight else None
+    codes, scale = _store(fmt, (Q, H), D)
+    st = _status()
+    L.csa_indexer_queries(x, pos, codes, scale, fmt=fmt, weight=w, norm=norm, rope_dims=rope, dev_status=st)
+    _sync(st)
+    y = io.norm_rope(f64(x), pos.cpu().numpy(), None if w is None else f64(w), norm=norm, rope=rope)
+    _same(codes, scale, _quant_ref(y, fmt))
+
+
+@pytest.mark.parametrize("fmt", [L.CSA_IDX_FP8, L.CSA_IDX_MXFP4])
+def test_indexer_queries_zero_and_non_finite_rows(fmt):
+    x = torch.randn((6, 4, 128), device=DEV)
+    x[0, 1] = 0
+    x[1, 2, 77] = float("nan")
+    x[2, 3, 3] = float("inf")
+    x[3, 0] *= 1e-30
+    x[4, 0] *= 1e30
+    pos = torch.arange(6, dtype=torch.int32, device=DEV)
+    for norm in (True, False):
+        codes, scale = _store(fmt, (6, 4), 128)
+        st = _status()
+        L.csa_indexer_queries(x, pos, codes, scale, fmt=fmt, norm=norm, dev_status=st)
+        _sync(st, L.CSA_DEV_NAN)
+        _same(codes, scale, _quant_ref(io.norm_rope(f64(x), pos.cpu().numpy(), norm=norm), fmt))
+
+
+@pytest.mark.parametrize("fmt", [L.CSA_IDX_FP8, L.CSA_IDX_MXFP4])
+@pytest.mark.parametrize("D,dt,m,paged", [(128, "bf16", 4, True), (64, "f32", 4, True), (128, "f16", 4, False),
+                                          (64, "bf16", 128, False), (128, "f32", 128, False)])
+def test_indexer_append_bit_exact(D, dt, m, paged, fmt):
+    rng = np.random.default_rng(D + m)
+    T = [m * 70 + 3, m * 33, m - 1, m * 5 + 1]           # entries 70, 33, 0, 5
+    n_ent = [t // m for t in T]
+    items = [(b, i) for b, n in enumerate(n_ent) for i in range(n) if (b, i) not in ((0, 3), (1, 0))]
+    rng.shuffle(items)
+    bad = [(0, 70), (2, 0), (3, 6), (4, 0), (-1, 0), (1, -1), (0, 2 ** 31 - 1)]
+    items = items[:20] + bad + items[20:]
+    seq, ent = (np.array([x[j] for x in items], np.int32) for j in (0, 1))
+    k = _gpu(rng.standard_normal((len(items), D + 8)).astype(np.float32), DT[dt])[:, :D]
+    w = _gpu((1 + 0.1 * rng.standard_normal(D)).astype(np.float32))
+    if paged:
+        table = rng.permutation(12).astype(np.int32).reshape(4, 3)
+        row = lambda b, i: int(table[b, i // 32]) * 32 + i % 32  # noqa: E731
+        rows, off, layout = 12 * 32, None, L.cache_layout(_gpu(table))
+    else:
+        o = np.concatenate([[5], 5 + np.cumsum(n_ent)[:-1] + 3]).astype(np.int64)
+        row = lambda b, i: int(o[b]) + i  # noqa: E731
+        rows, off, layout = sum(n_ent) + 20, _gpu(o), None
+    codes, scale = _store(fmt, (rows,), D)
+    want_c, want_s = codes.cpu().numpy(), scale.cpu().numpy()
+    st = _status()
+    L.csa_indexer_append(k, _gpu(np.array(T, np.int64)), off, _gpu(seq), _gpu(ent), codes, scale, B=4, m=m,
+                         fmt=fmt, weight=w, layout=layout, dev_status=st)
+    _sync(st, L.CSA_DEV_OOB)
+    ok = np.array([0 <= b < 4 and 0 <= i < n_ent[b] for b, i in items])
+    y = io.norm_rope(f64(k)[ok][:, None], (ent[ok].astype(np.int64) + 1) * m - 1, f64(w))[:, 0]
+    at = [row(b, i) for (b, i), g in zip(items, ok) if g]
+    want_c[at], want_s[at] = _quant_ref(y, fmt)
+    _same(codes, scale, (want_c, want_s))
+
+
+def test_indexer_append_bad_blocks_are_skipped():
+    # block table entries that are unset, or whose rows lie past the store; a sequence longer
+    # than its table
+    table = torch.tensor([[0, -1, 5, 2]], dtype=torch.int32, device=DEV)
+    codes, scale = _store(L.CSA_IDX_FP8, (3 * 32,), 128)
+    k = torch.randn((5, 128), device=DEV)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    st = _status()
+    L.csa_indexer_append(k, torch.tensor([4000], device=DEV), None, i32(0, 0, 0, 0, 0), i32(3, 40, 70, 100, 130),
+                         codes, scale, B=1, layout=L.cache_layout(table), dev_status=st)
+    _sync(st, L.CSA_DEV_OOB)
+    written = (scale != 0.5).nonzero().flatten().tolist()
+    assert written == [3, 2 * 32 + 4]
+
+
+def test_other_stream_and_current_device():
+    s = torch.cuda.Stream()
+    x = torch.randn((64, 256), device=DEV)
+    codes, sf = torch.zeros((64, 128), dtype=torch.uint8, device=DEV), _sf_empty(64, 256, 0)
+    s.wait_stream(torch.cuda.current_stream())
+    L.csa_mxfp4_quantize(x, codes, sf, stream=s)
+    with torch.cuda.stream(s):
+        out = torch.empty_like(x)
+        L.csa_mxfp4_dequantize(codes, sf, out)
+    s.synchronize()
+    p, b = io.mxfp4(f64(x))
+    assert np.array_equal(f64(out), io.mxfp4_values(p, b))
+
+
+def test_empty_calls_launch_nothing():
+    n0 = L.csa_launch_count()
+    u8 = lambda *n: torch.empty(n, dtype=torch.uint8, device=DEV)  # noqa: E731
+    L.csa_mxfp4_quantize(torch.empty((0, 64), device=DEV), u8(0, 32), u8(0, 2))
+    L.csa_mxfp4_matmul(u8(0, 32), u8(0), u8(8, 32), u8(512), torch.empty((0, 8), device=DEV))
+    e32 = torch.empty(0, dtype=torch.int32, device=DEV)
+    L.csa_qk_norm_rope(torch.empty((0, 4, 64), device=DEV), None, e32, torch.empty((0, 4, 64), device=DEV), None)
+    L.csa_indexer_queries(torch.empty((0, 4, 64), device=DEV), e32, u8(0, 4, 64), torch.empty((0, 4), device=DEV))
+    L.csa_indexer_append(torch.empty((0, 64), device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV),
+                         torch.zeros(1, dtype=torch.int64, device=DEV), e32, e32, u8(4, 64),
+                         torch.empty(4, device=DEV), B=1)
+    torch.cuda.synchronize()
+    assert L.csa_launch_count() == n0

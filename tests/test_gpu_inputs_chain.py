@@ -1,0 +1,208 @@
+"""The operators that make the indexer's inputs, run together as a layer runs them: hidden
+states through the MXFP4 query projection, the heads' norm, rotation and quantisation; keys
+appended to the hybrid cache's blocks; selection and attention on what they wrote.
+
+Codes are compared bit for bit with the 64-bit forms, and the index sets and outputs with the same
+selection and attention on the 64-bit forms' codes in a contiguous store.  The
+projection's inputs keep fp32 sums exact (K = 256 and block exponents within a few binades:
+multiples of 2^-6 below 2^14), so nothing between the hidden states and the codes rounds twice."""
+import numpy as np
+import pytest
+import torch
+
+import _inputs_orc as io
+import long_context_compressed_04_b200 as L
+from long_context_compressed_04_b200 import cache, pipeline
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+K, HI, DI, D, H, TOPK = 256, 64, 128, 128, 64, 64
+
+
+def _hidden(g, n):
+    return torch.randn((n, K), generator=g, device=DEV).to(torch.bfloat16)
+
+
+def _f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _heads_ref(x, w, pos, head_w, fmt):
+    """The query heads' codes and scales in 64 bits."""
+    a, b = (io.mxfp4_values(*io.mxfp4(_f64(t))) for t in (x, w))
+    y = torch.from_numpy(a @ b.T).to(torch.bfloat16)
+    y = io.norm_rope(_f64(y).reshape(len(a), HI, DI), pos.cpu().numpy(), _f64(head_w))
+    return io.fp8(y) if fmt == L.CSA_IDX_FP8 else io.mxfp4(y)
+
+
+def _keys_ref(k, ent, key_w, fmt):
+    y = io.norm_rope(_f64(k)[:, None], (np.asarray(ent, np.int64) + 1) * 4 - 1, _f64(key_w))[:, 0]
+    return io.fp8(y) if fmt == L.CSA_IDX_FP8 else io.mxfp4(y)
+
+
+def _select(fmt, qI, qs, w, kI, ks, seq_len, off, q_seq, q_pos, idx, max_n):
+    ws = torch.empty(L.csa_indexer_workspace_size(q_seq.numel(), max_n, TOPK), dtype=torch.uint8, device=DEV)
+    fn = L.lightning_indexer_topk if fmt == L.CSA_IDX_FP8 else L.lightning_indexer_topk_mxfp4
+    fn(qI, qs, w, kI, ks, seq_len, off, q_seq, q_pos, idx, ws, B=seq_len.numel(), H_I=HI, d_I=DI, m=4,
+       k=TOPK, max_n=max_n)
+
+
+def _up(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+@pytest.mark.parametrize("fmt", [L.CSA_IDX_FP8, L.CSA_IDX_MXFP4])
+def test_decode_steps_match_the_64_bit_forms(fmt):
+    g = torch.Generator(device=DEV).manual_seed(17)
+    T0, S = [1001, 130, 515], 9
+    B = len(T0)
+    Tmax = [t + S for t in T0]
+    n_max = [t // 4 for t in Tmax]
+    off = np.concatenate([[0], np.cumsum(n_max)[:-1]]).astype(np.int64)
+    head_w, key_w = (1 + 0.2 * torch.randn(DI, generator=g, device=DEV) for _ in range(2))
+    proj_w = (torch.randn((HI * DI, K), generator=g, device=DEV) / 16).to(torch.bfloat16)
+    keys = torch.randn((sum(n_max), DI), generator=g, device=DEV).to(torch.bfloat16)
+    kv, gate = (torch.randn((sum(Tmax), D), generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    kv_off = np.concatenate([[0], np.cumsum(Tmax)[:-1]]).astype(np.int64)
+    bias = torch.randn((8, D), generator=g, device=DEV) * 0.1
+    sink = torch.randn(H, generator=g, device=DEV)
+    kI_ref, ks_ref = _keys_ref(keys, np.concatenate([np.arange(n) for n in n_max]), key_w, fmt)
+    kI_lin, ks_lin = _up(kI_ref), _up(ks_ref)
+
+    proj = pipeline.QueryProjection(proj_w, HI, DI, max_q=8, fmt=fmt, head_weight=head_w)
+    hc = cache.HybridCache(B, D, 0, DI, n_blocks=40, max_blocks=12, device=DEV, idx_fmt=fmt)
+    hc.alloc.free = torch.randperm(40, generator=torch.Generator().manual_seed(5)).tolist()
+    for b, T in enumerate(T0):          # the prefix: raw tail, entries from their tokens, keys
+        r0, lo = int(kv_off[b]), max(T - 128, 0)
+        n = T // 4
+        ents = torch.zeros((n, 2 * D), dtype=torch.uint8, device=DEV)
+        i32 = torch.arange(n, dtype=torch.int32, device=DEV)
+        L.csa_compress(kv[r0:r0 + T], gate[r0:r0 + T], bias, torch.tensor([T], device=DEV),
+                       torch.zeros(1, dtype=torch.int64, device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV),
+                       torch.zeros(1, dtype=torch.int64, device=DEV), torch.zeros_like(i32), i32, ents, B=1, D=D)
+        hc.load_prefix(b, kv[r0 + lo:r0 + T], gate[r0 + lo:r0 + T], T, ents)
+        hc.append_keys((torch.full((n,), b, dtype=torch.int32, device=DEV), i32), keys[off[b]:off[b] + n], key_w)
+
+    q_seq = torch.arange(B, dtype=torch.int32, device=DEV)
+    for s in range(S):
+        p = [t + s for t in T0]
+        rows = torch.tensor([int(kv_off[b]) + p[b] for b in range(B)], device=DEV)
+        x = _hidden(g, B)
+        w = torch.rand((B, HI), generator=g, device=DEV)
+        q = torch.randn((B, H, D), generator=g, device=DEV).to(torch.bfloat16)
+        q_pos = torch.tensor(p, dtype=torch.int32, device=DEV)
+        # the step: append, compress and key the completed entries, project, select, attend
+        items = hc.append(kv[rows], gate[rows])
+        hc.compress(items, bias)
+        done = list(zip(items[0].tolist(), items[1].tolist()))
+        if done:
+            hc.append_keys(items, keys[torch.tensor([int(off[b]) + i for b, i in done], device=DEV)], key_w)
+        qI, qs = proj(x, q_pos)
+        L.csa_qk_norm_rope(q, None, q_pos, q, None, rope_dims=0)
+        idx = torch.full((B, TOPK), -1, dtype=torch.int32, device=DEV)
+        hc.select(qI, qs, w, q_seq, q_pos, idx, H_I=HI, k=TOPK)
+        out = torch.zeros((B, H, D), dtype=torch.bfloat16, device=DEV)
+        hc.attend(q, q_seq, q_pos, idx, sink, out, H=H, W=128, k=TOPK, softmax_scale=D ** -0.5)
+        torch.cuda.synchronize()
+        assert int(hc.dev_status.item()) == 0 and int(proj.dev_status.item()) == 0, s
+        ref = _heads_ref(x, proj_w, q_pos, head_w, fmt)
+        assert np.array_equal(qI.cpu().numpy(), ref[0]) and np.array_equal(qs.cpu().numpy(), ref[1]), s
+        # the same selection from a contiguous store of the 64-bit forms' codes
+        idx_ref = torch.full_like(idx, -1)
+        _select(fmt, _up(ref[0]), _up(ref[1]), w, kI_lin, ks_lin, torch.tensor([t + 1 for t in p], device=DEV),
+                _up(off), q_seq, q_pos, idx_ref, max(t + 1 for t in p) // 4)
+        assert torch.equal(idx, idx_ref), s
+        assert bool(out.isfinite().all())
+    # every key in its block
+    for b in range(B):
+        i = torch.arange(Tmax[b] // 4)
+        at = (hc.bt_host[b, i // 32].to(torch.int64) * 32 + i % 32).to(DEV)
+        e0 = int(off[b])
+        assert torch.equal(hc.kI[at], kI_lin[e0:e0 + len(i)]) and torch.equal(hc.ks[at], ks_lin[e0:e0 + len(i)])
+
+
+@pytest.mark.parametrize("fmt", [L.CSA_IDX_FP8, L.CSA_IDX_MXFP4])
+def test_captured_chain_replays_and_overlaps_exactly(fmt):
+    """Append, projection and selection as one graph, replayed on new inputs without a wait
+    in between, twice over the same buffers: each launch may start while its predecessor
+    finishes, and every replay has to give what separate, synchronised calls give."""
+    g = torch.Generator(device=DEV).manual_seed(23)
+    B, n, Q = 3, 700, 3
+    T = 4 * n
+    proj_w = (torch.randn((HI * DI, K), generator=g, device=DEV) / 16).to(torch.bfloat16)
+    proj = pipeline.QueryProjection(proj_w, HI, DI, max_q=Q, fmt=fmt)
+    seq_len = torch.full((B,), T, dtype=torch.int64, device=DEV)
+    off = torch.arange(B, dtype=torch.int64, device=DEV) * n
+    iseq = torch.arange(B, dtype=torch.int32, device=DEV).repeat_interleave(n)
+    ient = torch.arange(n, dtype=torch.int32, device=DEV).repeat(B)
+    kI = torch.zeros((B * n, DI if fmt == L.CSA_IDX_FP8 else DI // 2), dtype=torch.uint8, device=DEV)
+    ks = torch.zeros(B * n, device=DEV) if fmt == L.CSA_IDX_FP8 else \
+        torch.zeros((B * n, DI // 32), dtype=torch.uint8, device=DEV)
+    x, keys = _hidden(g, Q), torch.zeros((B * n, DI), dtype=torch.bfloat16, device=DEV)
+    w = torch.rand((Q, HI), generator=g, device=DEV)
+    q_seq = torch.arange(Q, dtype=torch.int32, device=DEV)
+    q_pos = torch.full((Q,), T - 1, dtype=torch.int32, device=DEV)
+    idx = torch.full((Q, TOPK), -1, dtype=torch.int32, device=DEV)
+    ws = torch.empty(L.csa_indexer_workspace_size(Q, n, TOPK), dtype=torch.uint8, device=DEV)
+    fn = L.lightning_indexer_topk if fmt == L.CSA_IDX_FP8 else L.lightning_indexer_topk_mxfp4
+
+    def step():
+        L.csa_indexer_append(keys, seq_len, off, iseq, ient, kI, ks, B=B, fmt=fmt)
+        qI, qs = proj(x, q_pos)
+        fn(qI, qs, w, kI, ks, seq_len, off, q_seq, q_pos, idx, ws, B=B, H_I=HI, d_I=DI, m=4, k=TOPK, max_n=n)
+
+    data = [(_hidden(g, Q), torch.randn((B * n, DI), generator=g, device=DEV).to(torch.bfloat16))
+            for _ in range(6)]
+    want = []
+    for a, b in data:
+        x.copy_(a), keys.copy_(b)
+        step()
+        torch.cuda.synchronize()
+        want.append((idx.clone(), proj.codes.clone(), kI.clone()))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    for _ in range(2):                   # two graphs over the same workspaces
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=s):
+            step()
+            step()                       # overwrites in place what the first one read
+        graphs.append(gr)
+    got = []
+    for r in range(12):
+        x.copy_(data[r % 6][0]), keys.copy_(data[r % 6][1])
+        graphs[r % 2].replay()
+        got.append((idx.clone(), proj.codes.clone(), kI.clone()))
+    torch.cuda.synchronize()
+    for r in range(12):
+        for a, b in zip(got[r], want[r % 6]):
+            assert torch.equal(a, b), r
+    # the same without a graph, calls back to back
+    got = []
+    for r in range(12):
+        x.copy_(data[r % 6][0]), keys.copy_(data[r % 6][1])
+        step()
+        step()
+        got.append((idx.clone(), proj.codes.clone(), kI.clone()))
+    torch.cuda.synchronize()
+    for r in range(12):
+        for a, b in zip(got[r], want[r % 6]):
+            assert torch.equal(a, b), r
+
+
+def test_projection_and_cache_refuse_what_they_cannot_hold():
+    w = torch.zeros((HI * DI, K), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="rows"):
+        pipeline.QueryProjection(w[1:], HI, DI, max_q=4)
+    proj = pipeline.QueryProjection(w, HI, DI, max_q=4)
+    pos = torch.zeros(5, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError, match="at most 4"):
+        proj(torch.zeros((5, K), dtype=torch.bfloat16, device=DEV), pos)
+    with pytest.raises(L.CSAError, match="q_pos"):
+        proj(torch.zeros((3, K), dtype=torch.bfloat16, device=DEV), pos)
+    with pytest.raises(ValueError, match="format"):
+        cache.HybridCache(1, 128, 0, 128, n_blocks=2, max_blocks=2, device=DEV, idx_fmt=7)
+    hc = cache.HybridCache(1, 128, 0, 128, n_blocks=2, max_blocks=2, device=DEV, idx_fmt=L.CSA_IDX_MXFP4)
+    z = torch.zeros((1, 128), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="append_keys"):
+        hc.append(z, z, z.to(torch.uint8), torch.zeros(1, device=DEV))
