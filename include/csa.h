@@ -491,10 +491,11 @@ csa_status_t csa_mxfp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uint8
  * csa_indexer_queries -- the same norm and rotation of the indexer's query heads, quantised.
  *   q [Q, H, D] in dtype (strides q_st, q_sh), q_pos int32 [Q]; codes and scale contiguous
  *   [Q, H, ..] in fmt (CSA_IDX_*; scale: fp32 [Q, H], or UE8M0 [Q, H, D / 32] bytes).
- *   D 64 or 128; rope_dims a multiple of 8, 0 .. D.  Computed in fp64 up to the rounding to
- *   codes, which are those of the definition whatever the batch.  A row (FP8) or block
- *   (MXFP4) that is not finite, or past the scale's range, gets a NaN scale and zero codes
- *   and sets CSA_DEV_NAN.
+ *   D 64 or 128; rope_dims a multiple of 8, 0 .. D.  The codes and the UE8M0 scales are those
+ *   of the definition in exact arithmetic (a value next to a rounding border is settled in
+ *   fp64), whatever the batch; an fp32 scale is within 2^-19 of it.  A row (FP8) or
+ *   block (MXFP4) that is not finite, or past the scale's range, gets a NaN scale and zero
+ *   codes and sets CSA_DEV_NAN.
  *
  * csa_indexer_append -- indexer keys of listed entries into the key store.
  *   Key n (row n of k [n_items, D], row stride k_ld) belongs to entry item_ent[n] of sequence

@@ -318,22 +318,25 @@ def dense_hca_attn(q, entries, seq_len, ent_off, kv, kv_off, kv_pos0, q_seq, q_p
 
 # ---- the lightning indexer's inputs --------------------------------------------------
 # These calls check their tensors' types, shapes and devices, since a wrong one would be
-# read past its end; sizes and alignments are checked by the library.
+# read past its end; sizes and alignments are checked by the library.  Each call tests all
+# of it in one expression of cheap accessors (decode steps issue many small launches, and
+# the host time per call is what bounds them); only a failed test looks for the reason.
 _DTYPES = {torch.bfloat16: CSA_DT_BF16, torch.float16: CSA_DT_F16, torch.float32: CSA_DT_F32}
+_U8, _I32T, _I64T, _F32T = torch.uint8, torch.int32, torch.int64, torch.float32
+# the raw handle without a Stream object (3 us less per call), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _bad(message: str):
     raise CSAError(1, message)
 
 
-def _rows_dtype(t, name):
-    d = _DTYPES.get(t.dtype)
-    if d is None:
+def _need_rows_dtype(t, name):
+    if t.dtype not in _DTYPES:
         _bad(f"{name} must be bfloat16, float16 or float32, not {t.dtype}")
-    return d
 
 
-def _dense(t, name, dtype, shape):
+def _need(t, name, dtype, shape):
     """A contiguous tensor of this type and shape (None in the shape: any size there)."""
     if t.dtype != dtype or not t.is_contiguous() or t.dim() != len(shape) or \
             any(n is not None and n != m for n, m in zip(shape, t.shape)):
@@ -342,106 +345,154 @@ def _dense(t, name, dtype, shape):
              f"{tuple(t.shape)} with strides {t.stride()}")
 
 
-def _on_device(*tensors):
-    """The device all given tensors are on, which must be the current one."""
+def _need_one_device(*tensors):
+    """All tensors on the current CUDA device."""
     dev = tensors[0].device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        _bad(f"tensors on {dev}: the current CUDA device is needed (torch.cuda.device)")
     for t in tensors:
         if t is not None and t.device != dev:
             _bad(f"tensors on {dev} and {t.device}")
-    return dev
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        _bad(f"tensors on {dev}: the current CUDA device is needed (torch.cuda.device)")
+
+
+def _need_status(dev_status):
+    if dev_status is not None and (dev_status.dtype != _I32T or dev_status.numel() < 1):
+        _bad("dev_status must be an int32 tensor of at least one element")
+
+
+def _need_2d(t, name):
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        _bad(f"{name} must be 2-D with contiguous rows, not {tuple(t.shape)} with strides "
+             f"{t.stride()}")
+
+
+def _is_current(dev):
+    return dev >= 0 and dev == torch.cuda.current_device()
+
+
+def _status_ok(t, dev):
+    return t is None or (t.dtype is _I32T and t.numel() >= 1 and t.get_device() == dev)
+
+
+def _rows_ok(t):
+    """2-D rows of a known type, contiguous along the last dimension."""
+    return t.dtype in _DTYPES and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)
+
+
+def _dense_ok(t, dtype, shape, dev):
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev
+
+
+def _weight_ok(w, D, dev):
+    return w is None or _dense_ok(w, _F32T, (D,), dev)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_of(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
-
-
-def _status_word(dev_status):
-    if dev_status is not None:
-        _dense(dev_status.view(-1), "dev_status", torch.int32, (None,))
-        if dev_status.numel() < 1:
-            _bad("dev_status needs one element")
-
-
-def _strided_2d(t, name):
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        _bad(f"{name} must be 2-D with contiguous rows, not {tuple(t.shape)} with strides "
-             f"{t.stride()}")
-    # a single row's stride is never used
-    return t.shape[0], t.shape[1], (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+def _stream_on(stream, dev):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(dev)
 
 
 def csa_mxfp4_sf_bytes(rows: int, cols: int, sf_layout: int = CSA_SF_ROWS) -> int:
     return _lib.csa_mxfp4_sf_bytes(rows, cols, sf_layout)
 
 
-def _mxfp4_pair(codes, sf, rows, cols, sf_layout, what):
-    _dense(codes, f"{what} codes", torch.uint8, (rows, cols // 2))
-    if sf.dtype != torch.uint8 or not sf.is_contiguous() or \
-            sf.numel() < _lib.csa_mxfp4_sf_bytes(rows, cols, sf_layout):
-        _bad(f"{what} scales must be a contiguous uint8 tensor of at least "
-             f"{_lib.csa_mxfp4_sf_bytes(rows, cols, sf_layout)} bytes")
+def _mxfp4_ok(codes, sf, rows, cols, sf_layout, dev):
+    need = (rows + 127) // 128 * ((cols + 127) // 128) * 512 if sf_layout else rows * (cols // 32)
+    return (codes.dtype is _U8 and codes.shape == (rows, cols // 2) and codes.is_contiguous()
+            and sf.dtype is _U8 and sf.numel() >= need and sf.is_contiguous()
+            and codes.get_device() == dev and sf.get_device() == dev)
+
+
+def _need_mxfp4(codes, sf, rows, cols, sf_layout, what):
+    _need(codes, f"{what} codes", _U8, (rows, cols // 2))
+    need = csa_mxfp4_sf_bytes(rows, cols, sf_layout)
+    if sf.dtype != _U8 or not sf.is_contiguous() or sf.numel() < need:
+        _bad(f"{what} scales must be a contiguous uint8 tensor of at least {need} bytes")
 
 
 def csa_mxfp4_quantize(x, codes, sf, *, sf_layout: int = CSA_SF_ROWS, dev_status=None,
                        stream=None):
     """Rows of x (bf16, fp16 or fp32 [rows, cols], any row stride) to packed e2m1 codes and
     UE8M0 scales in blocks of 32 (see include/csa.h)."""
-    rows, cols, ld = _strided_2d(x, "x")
-    dtype = _rows_dtype(x, "x")
-    _mxfp4_pair(codes, sf, rows, cols, sf_layout, "the")
-    _on_device(x, codes, sf, dev_status)
-    _status_word(dev_status)
-    _check(_lib.csa_mxfp4_quantize(x.data_ptr(), dtype, rows, cols, ld, codes.data_ptr(),
+    dev = x.get_device()
+    if not (_rows_ok(x) and _mxfp4_ok(codes, sf, *x.shape, sf_layout, dev)
+            and _status_ok(dev_status, dev) and _is_current(dev)):
+        _need_2d(x, "x")
+        _need_rows_dtype(x, "x")
+        _need_mxfp4(codes, sf, *x.shape, sf_layout, "the")
+        _need_status(dev_status)
+        _need_one_device(x, codes, sf, dev_status)
+    rows, cols = x.shape
+    _check(_lib.csa_mxfp4_quantize(x.data_ptr(), _DTYPES[x.dtype], rows, cols,
+                                   x.stride(0) if rows > 1 else cols, codes.data_ptr(),
                                    sf.data_ptr(), sf_layout, _ptr(dev_status),
-                                   _stream_of(stream)))
+                                   _stream_on(stream, dev)))
 
 
 def csa_mxfp4_dequantize(codes, sf, out, *, sf_layout: int = CSA_SF_ROWS, stream=None):
     """The values MXFP4 rows stand for, into out (bf16, fp16 or fp32 [rows, cols])."""
-    rows, cols, ld = _strided_2d(out, "out")
-    dtype = _rows_dtype(out, "out")
-    _mxfp4_pair(codes, sf, rows, cols, sf_layout, "the")
-    _on_device(codes, sf, out)
+    dev = out.get_device()
+    if not (_rows_ok(out) and _mxfp4_ok(codes, sf, *out.shape, sf_layout, dev)
+            and _is_current(dev)):
+        _need_2d(out, "out")
+        _need_rows_dtype(out, "out")
+        _need_mxfp4(codes, sf, *out.shape, sf_layout, "the")
+        _need_one_device(codes, sf, out)
+    rows, cols = out.shape
     _check(_lib.csa_mxfp4_dequantize(codes.data_ptr(), sf.data_ptr(), sf_layout, rows, cols,
-                                     out.data_ptr(), dtype, ld, _stream_of(stream)))
+                                     out.data_ptr(), _DTYPES[out.dtype],
+                                     out.stride(0) if rows > 1 else cols,
+                                     _stream_on(stream, dev)))
 
 
 def csa_mxfp4_matmul(a, a_sf, b, b_sf, out, *, dev_status=None, stream=None):
     """out[m, n] = sum_k A[m, k] B[n, k] of packed MXFP4 a [M, K / 2] and b [N, K / 2] with
     tiled scales (CSA_SF_TILED), out bf16, fp16 or fp32 [M, N] (any row stride)."""
-    M, N, ld = _strided_2d(out, "out")
-    dtype = _rows_dtype(out, "out")
+    dev = out.get_device()
     K = 2 * a.shape[-1]
-    _mxfp4_pair(a, a_sf, M, K, CSA_SF_TILED, "a's")
-    _mxfp4_pair(b, b_sf, N, K, CSA_SF_TILED, "b's")
-    _on_device(a, a_sf, b, b_sf, out, dev_status)
-    _status_word(dev_status)
+    if not (_rows_ok(out) and _mxfp4_ok(a, a_sf, out.shape[0], K, CSA_SF_TILED, dev)
+            and _mxfp4_ok(b, b_sf, out.shape[1], K, CSA_SF_TILED, dev)
+            and _status_ok(dev_status, dev) and _is_current(dev)):
+        _need_2d(out, "out")
+        _need_rows_dtype(out, "out")
+        _need_mxfp4(a, a_sf, out.shape[0], K, CSA_SF_TILED, "a's")
+        _need_mxfp4(b, b_sf, out.shape[1], K, CSA_SF_TILED, "b's")
+        _need_status(dev_status)
+        _need_one_device(a, a_sf, b, b_sf, out, dev_status)
+    M, N = out.shape
     _check(_lib.csa_mxfp4_matmul(a.data_ptr(), a_sf.data_ptr(), b.data_ptr(), b_sf.data_ptr(), M,
-                                 N, K, out.data_ptr(), dtype, ld, _ptr(dev_status),
-                                 _stream_of(stream)))
+                                 N, K, out.data_ptr(), _DTYPES[out.dtype],
+                                 out.stride(0) if M > 1 else N, _ptr(dev_status),
+                                 _stream_on(stream, dev)))
 
 
-def _heads(t, name, T, D):
-    """(pointer, token stride, head stride, heads) of [T, heads, D] rows."""
-    if t is None:
-        return None, 0, 0, 0
+def _need_heads(t, name, T, D):
     if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or (D > 1 and t.stride(2) != 1):
         _bad(f"{name} must be [{T}, heads, {D}] with contiguous channels, not {tuple(t.shape)} "
              f"with strides {t.stride()}")
+
+
+def _heads_ok(x, out, dtype, T, D, dev):
+    """Head rows [T, heads, D] and their output."""
+    return (x is None or (out is not None and x.dim() == 3 and x.shape == out.shape
+                          and x.shape[0] == T and x.shape[2] == D and x.dtype is dtype
+                          and out.dtype is dtype and x.get_device() == dev
+                          and out.get_device() == dev and x.stride(2) == 1
+                          and out.stride(2) == 1))
+
+
+def _head_strides(t, T):
+    """(pointer, token stride, head stride, heads); a lone token's or head's stride is unused."""
+    if t is None:
+        return None, 0, 0, 0
+    st, sh, _ = t.stride()
     n = t.shape[1]
-    return t.data_ptr(), (t.stride(0) if T > 1 else 0), (t.stride(1) if n > 1 else 0), n
-
-
-def _weight(w, name, D):
-    if w is not None:
-        _dense(w, name, torch.float32, (D,))
-    return _ptr(w)
+    return t.data_ptr(), (st if T > 1 else 0), (sh if n > 1 else 0), n
 
 
 def csa_qk_norm_rope(q, k, pos, q_out, k_out, *, q_weight=None, k_weight=None, norm: bool = True,
@@ -453,32 +504,52 @@ def csa_qk_norm_rope(q, k, pos, q_out, k_out, *, q_weight=None, k_weight=None, n
     lead = q if q is not None else k
     if lead is None:
         _bad("q and k are both None")
+    dev, dtype = lead.get_device(), lead.dtype
     T, D = lead.shape[0], lead.shape[-1]
-    dtype = _rows_dtype(lead, "q" if q is not None else "k")
-    qp, q_st, q_sh, H = _heads(q, "q", T, D)
-    kp, k_st, k_sh, Hk = _heads(k, "k", T, D)
-    qo, qo_st, qo_sh, Ho = _heads(q_out if q is not None else None, "q_out", T, D)
-    ko, ko_st, ko_sh, Hko = _heads(k_out if k is not None else None, "k_out", T, D)
-    if Ho != H or Hko != Hk:
-        _bad("q_out and k_out must have the heads of q and k")
-    for t in (k, q_out, k_out):
-        if t is not None and t.dtype != lead.dtype:
-            _bad("q, k and their outputs must have one element type")
-    _dense(pos, "pos", torch.int32, (T,))
-    qw, kw = _weight(q_weight, "q_weight", D), _weight(k_weight, "k_weight", D)
-    _on_device(lead, k, pos, q_out, k_out, q_weight, k_weight)
-    _check(_lib.csa_qk_norm_rope(qp, q_st, q_sh, kp, k_st, k_sh, pos.data_ptr(), qw, kw, qo, qo_st,
-                                 qo_sh, ko, ko_st, ko_sh, dtype, T, H, Hk, D, rope_dims,
-                                 1 if norm else 0, rope_theta, eps, _stream_of(stream)))
+    if not (dtype in _DTYPES and _heads_ok(q, q_out, dtype, T, D, dev)
+            and _heads_ok(k, k_out, dtype, T, D, dev) and _dense_ok(pos, _I32T, (T,), dev)
+            and _weight_ok(q_weight, D, dev) and _weight_ok(k_weight, D, dev)
+            and _is_current(dev)):
+        _need_rows_dtype(lead, "q" if q is not None else "k")
+        for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+            if x is None:
+                continue
+            _need_heads(x, name, T, D)
+            if out is None or out.dim() != 3 or out.shape[1] != x.shape[1]:
+                _bad("q_out and k_out must have the heads of q and k")
+            _need_heads(out, f"{name}_out", T, D)
+            if x.dtype != dtype or out.dtype != dtype:
+                _bad("q, k and their outputs must have one element type")
+        _need(pos, "pos", _I32T, (T,))
+        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if w is not None:
+                _need(w, name, _F32T, (D,))
+        _need_one_device(lead, k, pos, None if q is None else q_out, None if k is None else k_out,
+                         q_weight, k_weight)
+    qp, q_st, q_sh, H = _head_strides(q, T)
+    kp, k_st, k_sh, Hk = _head_strides(k, T)
+    qo, qo_st, qo_sh, _ = _head_strides(None if q is None else q_out, T)
+    ko, ko_st, ko_sh, _ = _head_strides(None if k is None else k_out, T)
+    _check(_lib.csa_qk_norm_rope(qp, q_st, q_sh, kp, k_st, k_sh, pos.data_ptr(), _ptr(q_weight),
+                                 _ptr(k_weight), qo, qo_st, qo_sh, ko, ko_st, ko_sh,
+                                 _DTYPES[dtype], T, H, Hk, D, rope_dims, 1 if norm else 0,
+                                 rope_theta, eps, _stream_on(stream, dev)))
 
 
-def _indexer_rows(codes, scale, lead, D, fmt):
+def _indexer_rows_ok(codes, scale, lead, D, fmt, dev):
     if fmt == CSA_IDX_FP8:
-        _dense(codes, "codes", torch.uint8, (*lead, D))
-        _dense(scale, "scale", torch.float32, lead)
+        return _dense_ok(codes, _U8, (*lead, D), dev) and _dense_ok(scale, _F32T, lead, dev)
+    return _dense_ok(codes, _U8, (*lead, D // 2), dev) and \
+        _dense_ok(scale, _U8, (*lead, D // 32), dev)
+
+
+def _need_indexer_rows(codes, scale, lead, D, fmt):
+    if fmt == CSA_IDX_FP8:
+        _need(codes, "codes", _U8, (*lead, D))
+        _need(scale, "scale", _F32T, lead)
     else:
-        _dense(codes, "codes", torch.uint8, (*lead, D // 2))
-        _dense(scale, "scale", torch.uint8, (*lead, D // 32))
+        _need(codes, "codes", _U8, (*lead, D // 2))
+        _need(scale, "scale", _U8, (*lead, D // 32))
 
 
 def csa_indexer_queries(q, q_pos, codes, scale, *, fmt: int = CSA_IDX_FP8, weight=None,
@@ -490,16 +561,23 @@ def csa_indexer_queries(q, q_pos, codes, scale, *, fmt: int = CSA_IDX_FP8, weigh
     if q.dim() != 3:
         _bad(f"q must be [Q, H, D], not {tuple(q.shape)}")
     Q, H, D = q.shape
-    dtype = _rows_dtype(q, "q")
-    qp, st, sh, _ = _heads(q, "q", Q, D)
-    _dense(q_pos, "q_pos", torch.int32, (Q,))
-    _indexer_rows(codes, scale, (Q, H), D, fmt)
-    w = _weight(weight, "weight", D)
-    _on_device(q, q_pos, codes, scale, weight, dev_status)
-    _status_word(dev_status)
-    _check(_lib.csa_indexer_queries(qp, dtype, st, sh, q_pos.data_ptr(), w, 1 if norm else 0,
-                                    rope_dims, rope_theta, eps, Q, H, D, fmt, codes.data_ptr(),
-                                    scale.data_ptr(), _ptr(dev_status), _stream_of(stream)))
+    dev = q.get_device()
+    if not (q.dtype in _DTYPES and q.stride(2) == 1 and _dense_ok(q_pos, _I32T, (Q,), dev)
+            and _indexer_rows_ok(codes, scale, (Q, H), D, fmt, dev) and _weight_ok(weight, D, dev)
+            and _status_ok(dev_status, dev) and _is_current(dev)):
+        _need_rows_dtype(q, "q")
+        _need_heads(q, "q", Q, D)
+        _need(q_pos, "q_pos", _I32T, (Q,))
+        _need_indexer_rows(codes, scale, (Q, H), D, fmt)
+        if weight is not None:
+            _need(weight, "weight", _F32T, (D,))
+        _need_status(dev_status)
+        _need_one_device(q, q_pos, codes, scale, weight, dev_status)
+    qp, st, sh, _ = _head_strides(q, Q)
+    _check(_lib.csa_indexer_queries(qp, _DTYPES[q.dtype], st, sh, q_pos.data_ptr(), _ptr(weight),
+                                    1 if norm else 0, rope_dims, rope_theta, eps, Q, H, D, fmt,
+                                    codes.data_ptr(), scale.data_ptr(), _ptr(dev_status),
+                                    _stream_on(stream, dev)))
 
 
 def csa_indexer_append(k, seq_len, ent_off, item_seq, item_ent, codes, scale, *, B: int,
@@ -509,22 +587,39 @@ def csa_indexer_append(k, seq_len, ent_off, item_seq, item_ent, codes, scale, *,
     """Indexer keys k [n, D] of the listed entries normed, rotated at their block ends,
     quantised and written to their rows of the key store (codes, scale), through the layout's
     block table or ent_off."""
-    n, D, ld = _strided_2d(k, "k")
-    dtype = _rows_dtype(k, "k")
-    _dense(item_seq, "item_seq", torch.int32, (n,))
-    _dense(item_ent, "item_ent", torch.int32, (n,))
-    _dense(seq_len, "seq_len", torch.int64, (B,))
-    if ent_off is not None:
-        _dense(ent_off, "ent_off", torch.int64, (B,))
+    dev = k.get_device()
     bt = getattr(layout, "_block_table", None)
-    if bt is not None and (bt.dtype != torch.int32 or bt.dim() != 2 or bt.shape[0] < B):
-        _bad("the block table must be int32 [B, bt_stride]")
-    _indexer_rows(codes, scale, (codes.shape[0],), D, fmt)
-    w = _weight(weight, "weight", D)
-    _on_device(k, seq_len, ent_off, item_seq, item_ent, codes, scale, weight, bt, dev_status)
-    _status_word(dev_status)
-    _check(_lib.csa_indexer_append(k.data_ptr(), dtype, ld, seq_len.data_ptr(), _ptr(ent_off),
-                                   item_seq.data_ptr(), item_ent.data_ptr(), n, B, m, w,
-                                   1 if norm else 0, rope_dims, rope_theta, eps, D, fmt,
-                                   codes.data_ptr(), scale.data_ptr(), codes.shape[0],
-                                   _lay(layout), _ptr(dev_status), _stream_of(stream)))
+    if not (_rows_ok(k) and codes.dim() == 2
+            and _indexer_rows_ok(codes, scale, (codes.shape[0],), k.shape[1], fmt, dev)
+            and _dense_ok(item_seq, _I32T, k.shape[:1], dev)
+            and _dense_ok(item_ent, _I32T, k.shape[:1], dev)
+            and _dense_ok(seq_len, _I64T, (B,), dev)
+            and (ent_off is None or _dense_ok(ent_off, _I64T, (B,), dev))
+            and (bt is None or (bt.dtype is _I32T and bt.dim() == 2 and bt.shape[0] >= B
+                                and bt.stride(1) == 1 and bt.get_device() == dev))
+            and _weight_ok(weight, k.shape[1], dev) and _status_ok(dev_status, dev)
+            and _is_current(dev)):
+        _need_2d(k, "k")
+        _need_rows_dtype(k, "k")
+        n, D = k.shape
+        _need(item_seq, "item_seq", _I32T, (n,))
+        _need(item_ent, "item_ent", _I32T, (n,))
+        _need(seq_len, "seq_len", _I64T, (B,))
+        if ent_off is not None:
+            _need(ent_off, "ent_off", _I64T, (B,))
+        if bt is not None and (bt.dtype != _I32T or bt.dim() != 2 or bt.shape[0] < B
+                               or (bt.shape[1] > 1 and bt.stride(1) != 1)):
+            _bad("the block table must be int32 [B, bt_stride] with contiguous rows")
+        _need_indexer_rows(codes, scale, (codes.shape[0],), D, fmt)
+        if weight is not None:
+            _need(weight, "weight", _F32T, (D,))
+        _need_status(dev_status)
+        _need_one_device(k, seq_len, ent_off, item_seq, item_ent, codes, scale, weight, bt,
+                         dev_status)
+    n, D = k.shape
+    _check(_lib.csa_indexer_append(k.data_ptr(), _DTYPES[k.dtype], k.stride(0) if n > 1 else D,
+                                   seq_len.data_ptr(), _ptr(ent_off), item_seq.data_ptr(),
+                                   item_ent.data_ptr(), n, B, m, _ptr(weight), 1 if norm else 0,
+                                   rope_dims, rope_theta, eps, D, fmt, codes.data_ptr(),
+                                   scale.data_ptr(), codes.shape[0], _lay(layout),
+                                   _ptr(dev_status), _stream_on(stream, dev)))

@@ -41,31 +41,103 @@ __device__ __forceinline__ void rotation(double pos, double freq, double& c, dou
 
 // ---- rows kept in their type -------------------------------------------------------------
 struct QkArgs {
-    const void* q;
-    const void* k;
-    void* q_out;
-    void* k_out;
-    const float* q_weight;
-    const float* k_weight;
+    QkRows q, k;
     const int32_t* pos;
-    int64_t q_st, q_sh, k_st, k_sh, qo_st, qo_sh, ko_st, ko_sh;   // strides, elements
-    int T, H, Hk, D, rope, norm;
+    int T, D, rope, norm;
     int heads_per_warp, warps_per_token;
     float eps;
 };
+
+__device__ __forceinline__ void load_weight8(const float* weight, int ch, float* w) {
+    if (weight) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(weight + ch));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(weight + ch + 4));
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) w[j] = 1.f;
+    }
+}
+
+// Heads [h0, h1) of one token, kU passes of 32 / LPR rows at a time: the loads of all kU go
+// out before the first is used.
+template <class T, int LPR, int C, int kU>
+__device__ __forceinline__ void norm_rope_heads(const QkRows& x, int64_t t, int h0, int h1, int D,
+                                                int lo, bool norm, float eps, int sub, int l,
+                                                const float (&cs)[C][4], const float (&sn)[C][4]) {
+    constexpr int kRows = 32 / LPR;
+    float w[C][8];
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+        const int ch = 8 * (l + LPR * c);
+        load_weight8(ch < D ? x.weight : nullptr, ch, w[c]);
+    }
+    const float inv_d = 1.f / (float)D;
+    const T* src = (const T*)x.x + t * x.st + (h0 + sub) * x.sh + 8 * l;
+    T* dst = (T*)x.out + t * x.ost + (h0 + sub) * x.osh + 8 * l;
+    for (int hb = h0 + sub; hb - sub < h1; hb += kU * kRows) {
+        Row8<T> r[kU][C];
+#pragma unroll
+        for (int u = 0; u < kU; u++)
+#pragma unroll
+            for (int c = 0; c < C; c++) {
+                r[u][c].zero();
+                if (hb + u * kRows < h1 && 8 * (l + LPR * c) < D)
+                    r[u][c].load(src + u * kRows * x.sh + 8 * LPR * c);
+            }
+#pragma unroll
+        for (int u = 0; u < kU; u++) {
+            float f[C][8];
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int c = 0; c < C; c++) {
+                r[u][c].get(f[c]);
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    s0 = fmaf(f[c][j], f[c][j], s0);
+                    s1 = fmaf(f[c][j + 1], f[c][j + 1], s1);
+                }
+            }
+            float rs = 1.f;
+            if (norm) rs = rsqrtf(fmaf(group_sum<LPR>(s0 + s1), inv_d, eps));
+            const bool in = hb + u * kRows < h1;
+#pragma unroll
+            for (int c = 0; c < C; c++) {
+                const int ch = 8 * (l + LPR * c);
+#pragma unroll
+                for (int j = 0; j < 8; j++) f[c][j] *= rs * w[c][j];
+                if (ch + 8 > lo) {
+#pragma unroll
+                    for (int p = 0; p < 4; p++) {
+                        const float a = f[c][2 * p], b = f[c][2 * p + 1];
+                        // a chunk may hold the border: its first pairs stay as they are
+                        if (ch >= lo || ch + 2 * p >= lo) {
+                            f[c][2 * p] = a * cs[c][p] - b * sn[c][p];
+                            f[c][2 * p + 1] = a * sn[c][p] + b * cs[c][p];
+                        }
+                    }
+                }
+                Row8<T> o;
+                o.set(f[c]);
+                if (in && ch < D) o.store(dst + u * kRows * x.osh + 8 * LPR * c);
+            }
+        }
+        src += kU * kRows * x.sh;
+        dst += kU * kRows * x.osh;
+    }
+}
 
 // LPR lanes a row, C chunks of 8 channels a lane (chunk c of lane l: channels 8 (l + LPR c)).
 template <class T, int LPR, int C>
 __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const QkArgs a, const RopeTable rt) {
     pdl_wait();
     const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
-    constexpr int kRows = 32 / LPR;
     const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int64_t t = task / a.warps_per_token;
     if (t >= a.T) return;
-    const int h0 = (int)(task % a.warps_per_token) * a.heads_per_warp;
-    const int heads = a.H + a.Hk;
-    const int h1 = min(h0 + a.heads_per_warp, heads);
+    const int h0 = (int)(task - t * a.warps_per_token) * a.heads_per_warp;
+    const int h1 = min(h0 + a.heads_per_warp, a.q.heads + a.k.heads);
     const int lo = a.D - a.rope;              // first rotated channel (even)
     float cs[C][4], sn[C][4];
     const double pos = (double)a.pos[t];
@@ -84,68 +156,36 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const QkArgs 
             }
         }
     }
-    for (int hb = h0; hb < h1; hb += kRows) {
-        const int h = hb + sub;
-        const bool in = h < h1;
-        const bool isq = h < a.H;
-        const T* src = isq ? (const T*)a.q + t * a.q_st + h * a.q_sh
-                           : (const T*)a.k + t * a.k_st + (h - a.H) * a.k_sh;
-        Row8<T> r[C];
-        float ss = 0.f;
-#pragma unroll
-        for (int c = 0; c < C; c++) {
-            const int ch = 8 * (l + LPR * c);
-            r[c].zero();
-            if (in && ch < a.D) r[c].load(src + ch);
-        }
-#pragma unroll
-        for (int c = 0; c < C; c++) {
-            float f[8];
-            r[c].get(f);
-#pragma unroll
-            for (int j = 0; j < 8; j++) ss = fmaf(f[j], f[j], ss);
-        }
-        float rs = 1.f;
-        if (a.norm) rs = rsqrtf(group_sum<LPR>(ss) / (float)a.D + a.eps);
-        if (!in) continue;
-        const float* w = isq ? a.q_weight : a.k_weight;
-        T* dst = isq ? (T*)a.q_out + t * a.qo_st + h * a.qo_sh
-                     : (T*)a.k_out + t * a.ko_st + (h - a.H) * a.ko_sh;
-#pragma unroll
-        for (int c = 0; c < C; c++) {
-            const int ch = 8 * (l + LPR * c);
-            if (ch >= a.D) continue;
-            float f[8];
-            r[c].get(f);
-            if (w) {
-                const float4 w0 = __ldg(reinterpret_cast<const float4*>(w + ch));
-                const float4 w1 = __ldg(reinterpret_cast<const float4*>(w + ch + 4));
-                const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-                for (int j = 0; j < 8; j++) f[j] *= rs * ww[j];
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; j++) f[j] *= rs;
-            }
-#pragma unroll
-            for (int p = 0; p < 4; p++) {
-                if (ch + 2 * p < lo) continue;
-                const float x = f[2 * p], y = f[2 * p + 1];
-                f[2 * p] = x * cs[c][p] - y * sn[c][p];
-                f[2 * p + 1] = x * sn[c][p] + y * cs[c][p];
-            }
-            Row8<T> o;
-            o.set(f);
-            o.store(dst + ch);
-        }
-    }
+    constexpr int kU = C == 1 ? 4 : 1;
+    if (h0 < a.q.heads)
+        norm_rope_heads<T, LPR, C, kU>(a.q, t, h0, min(h1, a.q.heads), a.D, lo, a.norm, a.eps, sub, l, cs, sn);
+    if (h1 > a.q.heads)
+        norm_rope_heads<T, LPR, C, 1>(a.k, t, max(h0 - a.q.heads, 0), h1 - a.q.heads, a.D, lo, a.norm, a.eps,
+                                      sub, l, cs, sn);
     __threadfence();   // visible before the next kernel's reads ahead of its own wait
 }
 
 // ---- rows in the indexer's stored formats ----------------------------------------------------
-// The arithmetic is fp64 from the input's bits to the code: an e4m3 or e2m1 code (and a
-// block's power-of-two scale) next to a rounding border would depend on the order of fp32
-// sums, and the index sets with it.  In fp64 the codes are those of the definition.
+// The codes are those of the definition, whatever the order of the sums: an e4m3 or e2m1 code
+// (or a block's power-of-two scale) next to a rounding border is not left to fp32.  The fast
+// path computes in fp32 and brackets every quotient z by its error bound: if the codes of z -
+// margin and z + margin agree, that code is the one.  If they differ anywhere in the warp's
+// rows (about 1 pass in 300 for MXFP4, 1 in 80 for e4m3, on normal data), or the values
+// leave the range the bound holds in, the rows are done again in fp64.
+//
+// The bound, u = 2^-24, relative to |y| (|y1| + |y2| in a rotated pair): the sum of squares
+// takes at most 5 roundings in a lane and log2(LPR) <= 4 across, with eps 10 u, of which rsqrt
+// halves 5 u and adds its 2 ulp = 4 u; the products with weight and x add 2 u, cos and sin u,
+// the rotation's product, sum and the rounding of its result 3 u: 15 u.  The bracket's
+// own rounding adds u: 16 u < kFp4Margin.  The e4m3 quotient is y * (448 / max|y|), in which r
+// cancels: 6 u of y, twice 6 u of the largest |y| (|y1| + |y2| <= 2 max), 2 u of the quotient
+// and the product, 1 u of the bracket: 21 u < kFp8Margin.  In both, |z| is at most the
+// bracketed magnitude.  Between 2^-60 and 2^120 an underflowed product is below 2^-34 of a
+// quotient's unit, far from every border but zero's, whose sign it keeps.
+constexpr float kU24 = 5.9604645e-08f;
+constexpr float kFp4Margin = 20.f * kU24;
+constexpr float kFp8Margin = 24.f * kU24;
+
 struct RowQuant {
     uint8_t* codes;    // rows of D (e4m3) or D / 2 (e2m1) bytes
     float* scale;      // e4m3: one fp32 per row
@@ -153,37 +193,45 @@ struct RowQuant {
     int32_t* st;
 };
 
-// One row over LPR = D / 8 lanes (all lanes of the warp call it): norm, rotation (cs, sn of
-// this lane's 4 pairs), codes and scale to row `dst`.
+// A row's result in a lane: its 8 codes (4 bytes for e2m1) and scale, and whether it is bad.
+struct RowCodes {
+    uint32_t c0, c1;
+    uint32_t scale;    // fp32 bits, or the UE8M0 byte
+    bool bad;
+};
+
+struct Eight {
+    float v[8];
+};
+
+// The row in fp64 from the input's bits to the codes.  Out of line, its arguments by value: an
+// array whose address is taken would live in local memory on the fast path too.
 template <int LPR, bool FP4>
-__device__ __forceinline__ void quantize_row(const float* x, int l, const double* cs,
-                                             const double* sn, bool rot, const float* w, bool norm,
-                                             double eps, const RowQuant& o, int64_t dst, bool in) {
+__device__ __noinline__ RowCodes quantize_row_f64(const Eight x, const Eight w, const double2* rot, bool norm,
+                                                  double eps) {
     constexpr int D = 8 * LPR;
     double y[8];
-    double r = 1.0;
-    if (norm) {
-        double ss = 0.0;
+    double ss = 0.0;
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            y[j] = (double)x[j];
-            ss = fma(y[j], y[j], ss);
-        }
-        r = rsqrt(group_sum<LPR>(ss) * (1.0 / D) + eps);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++) y[j] = (double)x[j];
+    for (int j = 0; j < 8; j++) {
+        y[j] = (double)x.v[j];
+        ss = fma(y[j], y[j], ss);
     }
+    double r = 1.0;
+    if (norm) r = rsqrt(group_sum<LPR>(ss) * (1.0 / D) + eps);
 #pragma unroll
-    for (int j = 0; j < 8; j++) y[j] *= r * (double)w[j];
+    for (int j = 0; j < 8; j++) y[j] *= r * (double)w.v[j];
     if (rot) {
 #pragma unroll
         for (int p = 0; p < 4; p++) {
-            const double u = y[2 * p], v = y[2 * p + 1];
-            y[2 * p] = u * cs[p] - v * sn[p];
-            y[2 * p + 1] = u * sn[p] + v * cs[p];
+            const double2 cs = rot[p];
+            const double a = y[2 * p], b = y[2 * p + 1];
+            y[2 * p] = a * cs.x - b * cs.y;
+            y[2 * p + 1] = a * cs.y + b * cs.x;
         }
     }
+    RowCodes o;
+    float f[8];
     if constexpr (FP4) {
         // the block's scale needs the exponent of its largest magnitude only
         int top = 0;
@@ -192,20 +240,14 @@ __device__ __forceinline__ void quantize_row(const float* x, int l, const double
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int ex = (top >> 20) - 1023;              // floor(log2(amax)); -1023 for zeros
-        const bool bad = ex > 129;                      // not finite, or past the scales' range
-        const int e = bad ? 255 : max(ex - 2 + 127, 0);
-        const double inv = __hiloint2double((1023 + 127 - (bad ? 127 : e)) << 20, 0);
-        float f[8];
+        o.bad = ex > 129;                               // not finite, or past the scales' range
+        const int e = o.bad ? 255 : max(ex - 2 + 127, 0);
+        const double inv = __hiloint2double((1023 + 127 - (o.bad ? 127 : e)) << 20, 0);
 #pragma unroll
-        for (int j = 0; j < 8; j++) f[j] = f64_to_f32_odd(bad ? 0.0 : y[j] * inv);
-        const uint32_t c = pack_e2m1x8(f);
-        if (in) {
-            reinterpret_cast<uint32_t*>(o.codes)[dst * (D / 8) + l] = c;
-            if ((l & 3) == 0) {
-                o.sf[dst * (D / 32) + (l >> 2)] = (uint8_t)e;
-                if (bad) flag(o.st, CSA_DEV_NAN);
-            }
-        }
+        for (int j = 0; j < 8; j++) f[j] = f64_to_f32_odd(o.bad ? 0.0 : y[j] * inv);
+        o.c0 = pack_e2m1x8(f);
+        o.c1 = 0;
+        o.scale = (uint32_t)e;
     } else {
         double top = 0.0;
         bool nan = false;
@@ -215,42 +257,155 @@ __device__ __forceinline__ void quantize_row(const float* x, int l, const double
             nan |= y[j] != y[j];
         }
 #pragma unroll
-        for (int s = LPR / 2; s > 0; s >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, s));
-        float scale = (float)(top * (1.0 / 448.0));
-        const unsigned group = (LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1u)) << ((threadIdx.x & 31) & ~(LPR - 1));
-        const bool bad = (__ballot_sync(0xffffffffu, nan) & group) != 0 || !(scale <= 3.402823466e38f);
-        if (!(scale > 0.f)) scale = 1.f;
+        for (int s = LPR / 2; s > 0; s >>= 1) {
+            top = fmax(top, __shfl_xor_sync(0xffffffffu, top, s));
+            nan |= __shfl_xor_sync(0xffffffffu, (int)nan, s) != 0;
+        }
+        float scale = (float)(top / 448.0);
+        o.bad = nan || !(scale <= 3.402823466e38f);
+        if (!(scale > 0.f) || o.bad) scale = 1.f;
         // y / scale: the product with the rounded reciprocal, mended once by its remainder, so
         // that a quotient fp64 holds (a tie between two codes, say) comes out exactly
         const double sd = (double)scale, inv = 1.0 / sd;
-        float f[8];
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             const double z = y[j] * inv;
-            f[j] = f64_to_f32_odd(bad ? 0.0 : fma(fma(-z, sd, y[j]), inv, z));
+            f[j] = f64_to_f32_odd(o.bad ? 0.0 : fma(fma(-z, sd, y[j]), inv, z));
         }
         const uint2 c = pack_e4m3x8(f);
-        if (in) {
-            reinterpret_cast<uint2*>(o.codes)[dst * LPR + l] = c;
-            if (l == 0) {
-                o.scale[dst] = bad ? __int_as_float(0x7fffffff) : scale;
-                if (bad) flag(o.st, CSA_DEV_NAN);
-            }
+        o.c0 = c.x;
+        o.c1 = c.y;
+        o.scale = o.bad ? 0x7fffffffu : __float_as_uint(scale);
+    }
+    return o;
+}
+
+// One row over LPR = D / 8 lanes (all lanes of the warp call it): norm, rotation (cs, sn of
+// this lane's 4 pairs where rot is given, rot the same in fp64), codes and scale to row `dst`.
+template <int LPR, bool FP4>
+__device__ __forceinline__ void quantize_row(const float* x, int l, const float* cs, const float* sn,
+                                             const double2* rot, const float* w, bool norm, float eps,
+                                             const RowQuant& o, int64_t dst, bool in) {
+    constexpr int D = 8 * LPR;
+    float r = 1.f;
+    bool near = false;          // not settled in fp32
+    if (norm) {
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            s0 = fmaf(x[j], x[j], s0);
+            s1 = fmaf(x[j + 1], x[j + 1], s1);
+        }
+        const float ms = fmaf(group_sum<LPR>(s0 + s1), 1.f / D, eps);
+        near = !(ms > 8.6736174e-19f && ms < 1.2676506e+30f);    // 2^-60, 2^100
+        r = rsqrtf(ms);
+    }
+    float y[8], mag[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        y[j] = x[j] * (r * w[j]);
+        mag[j] = fabsf(y[j]);
+    }
+    if (rot) {
+#pragma unroll
+        for (int p = 0; p < 4; p++) {
+            const float a = y[2 * p], b = y[2 * p + 1];
+            mag[2 * p] = mag[2 * p + 1] = fabsf(a) + fabsf(b);
+            y[2 * p] = fmaf(a, cs[p], -(b * sn[p]));
+            y[2 * p + 1] = fmaf(a, sn[p], b * cs[p]);
+        }
+    }
+    uint32_t top = 0;           // as bits: a NaN is above all
+#pragma unroll
+    for (int j = 0; j < 8; j++) top = max(top, __float_as_uint(y[j]) & 0x7fffffffu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    if constexpr (!FP4) {
+#pragma unroll
+        for (int s = 4; s < LPR; s <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
+    }
+    const float amax = __uint_as_float(top);
+    // 2^-60 .. 2^120, or a block of zeros
+    near |= top != 0u && !(amax > 8.6736174e-19f && amax < 1.3292280e+36f);
+    RowCodes c;
+    c.bad = false;
+    float inv, margin;
+    if constexpr (FP4) {
+        const uint32_t ex = top >> 23, e = ex > 2u ? ex - 2u : 0u;
+        // the largest magnitude may itself lie next to a power of two (|y1| + |y2| <= 2 amax)
+        near |= __float_as_uint(fmaf(amax, 2.1f * kFp4Margin, amax)) >> 23 != ex ||
+                __float_as_uint(fmaf(amax, -2.1f * kFp4Margin, amax)) >> 23 != ex;
+        inv = __uint_as_float((254u - min(e, 253u)) << 23);      // 2^(127 - e)
+        margin = kFp4Margin * inv;
+        c.scale = e;
+    } else {
+        inv = top ? 448.f / amax : 1.f;
+        margin = kFp8Margin * inv;
+        c.scale = __float_as_uint(top ? amax * (1.f / 448.f) : 1.f);
+    }
+    float lo[8], hi[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const float z = y[j] * inv;
+        lo[j] = fmaf(-mag[j], margin, z);
+        hi[j] = fmaf(mag[j], margin, z);
+    }
+    if constexpr (FP4) {
+        c.c0 = pack_e2m1x8(lo);
+        c.c1 = 0;
+        near |= pack_e2m1x8(hi) != c.c0;
+    } else {
+        const uint2 a = pack_e4m3x8(lo), b = pack_e4m3x8(hi);
+        c.c0 = a.x;
+        c.c1 = a.y;
+        near |= a.x != b.x || a.y != b.y;
+    }
+    if (__any_sync(0xffffffffu, near)) {
+        Eight xv, wv;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            xv.v[j] = x[j];
+            wv.v[j] = w[j];
+        }
+        c = quantize_row_f64<LPR, FP4>(xv, wv, rot, norm, (double)eps);
+    }
+    if (!in) return;
+    if constexpr (FP4) {
+        reinterpret_cast<uint32_t*>(o.codes)[dst * (D / 8) + l] = c.c0;
+        if ((l & 3) == 0) {
+            o.sf[dst * (D / 32) + (l >> 2)] = (uint8_t)c.scale;
+            if (c.bad) flag(o.st, CSA_DEV_NAN);
+        }
+    } else {
+        reinterpret_cast<uint2*>(o.codes)[dst * LPR + l] = make_uint2(c.c0, c.c1);
+        if (l == 0) {
+            o.scale[dst] = __uint_as_float(c.scale);
+            if (c.bad) flag(o.st, CSA_DEV_NAN);
         }
     }
 }
 
-template <class T>
-__device__ __forceinline__ void load_weight(const float* weight, int ch, float* w) {
-    if (weight) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(weight + ch));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(weight + ch + 4));
-        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-    } else {
+// This lane's 4 rotation pairs: fp32 in registers, fp64 in shared memory for the fp64 path
+// (nullptr where the lane's channels are not rotated).
+template <int LPR>
+__device__ __forceinline__ const double2* lane_rotation(double pos, const RopeTable& rt, int l, int rope,
+                                                        double2* mine, float* cs, float* sn) {
+    const int first = 4 * l - (8 * LPR - rope) / 2;
 #pragma unroll
-        for (int j = 0; j < 8; j++) w[j] = 1.f;
+    for (int p = 0; p < 4; p++) {
+        cs[p] = 1.f;
+        sn[p] = 0.f;
     }
+    if (first < 0) return nullptr;
+#pragma unroll
+    for (int p = 0; p < 4; p++) {
+        double c, s;
+        rotation(pos, rt.freq[first + p], c, s);
+        mine[p] = make_double2(c, s);
+        cs[p] = (float)c;
+        sn[p] = (float)s;
+    }
+    return mine;
 }
 
 struct QueryArgs {
@@ -260,41 +415,44 @@ struct QueryArgs {
     int64_t st, sh;           // strides of q, elements
     int Q, H, rope, norm;
     int heads_per_warp, warps_per_token;
-    double eps;
+    float eps;
     RowQuant o;
 };
 
 template <class T, int LPR, bool FP4>
 __global__ void __launch_bounds__(32 * kWarps) indexer_queries_kernel(const QueryArgs a, const RopeTable rt) {
+    __shared__ double2 rot64[32 * kWarps][4];
     pdl_wait();
     const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
-    constexpr int kRows = 32 / LPR, D = 8 * LPR;
+    constexpr int kRows = 32 / LPR;
     const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int64_t t = task / a.warps_per_token;
     if (t >= a.Q) return;
-    const int h0 = (int)(task % a.warps_per_token) * a.heads_per_warp;
+    const int h0 = (int)(task - t * a.warps_per_token) * a.heads_per_warp;
     const int h1 = min(h0 + a.heads_per_warp, a.H);
-    const T* src = (const T*)a.q + t * a.st + 8 * l;
-    float w[8];
-    load_weight<T>(a.weight, 8 * l, w);
-    const bool rot = 8 * l >= D - a.rope;
-    double cs[4], sn[4];
-    if (rot) {
-        const double pos = (double)a.pos[t];
+    float w[8], cs[4], sn[4];
+    load_weight8(a.weight, 8 * l, w);
+    const T* src = (const T*)a.q + t * a.st + (h0 + sub) * a.sh + 8 * l;
+    constexpr int kU = 2;                // rows a lane loads ahead of the one it works on
+    Row8<T> r[kU];
 #pragma unroll
-        for (int p = 0; p < 4; p++) rotation(pos, rt.freq[4 * l + p - (D - a.rope) / 2], cs[p], sn[p]);
+    for (int u = 0; u < kU; u++) {
+        r[u].zero();
+        if (h0 + sub + u * kRows < h1) r[u].load(src + u * kRows * a.sh);
     }
-    Row8<T> cur, nxt;
-    cur.zero();
-    if (h0 + sub < h1) cur.load(src + (h0 + sub) * a.sh);
+    const double2* rot = lane_rotation<LPR>((double)a.pos[t], rt, l, a.rope, rot64[threadIdx.x], cs, sn);
+    int64_t dst = t * a.H + h0 + sub;
     for (int hb = h0; hb < h1; hb += kRows) {
         const int h = hb + sub;
-        nxt.zero();
-        if (h + kRows < h1) nxt.load(src + (h + kRows) * a.sh);
         float x[8];
-        cur.get(x);
-        quantize_row<LPR, FP4>(x, l, cs, sn, rot, w, a.norm, a.eps, a.o, t * a.H + h, h < h1);
-        cur = nxt;
+        r[0].get(x);
+#pragma unroll
+        for (int u = 0; u + 1 < kU; u++) r[u] = r[u + 1];
+        r[kU - 1].zero();
+        src += kRows * a.sh;
+        if (h + kU * kRows < h1) r[kU - 1].load(src + (kU - 1) * kRows * a.sh);
+        quantize_row<LPR, FP4>(x, l, cs, sn, rot, w, a.norm, a.eps, a.o, dst, h < h1);
+        dst += kRows;
     }
     __threadfence();
 }
@@ -309,16 +467,17 @@ struct AppendArgs {
     const int32_t* item_ent;
     int64_t n, ent_rows;
     int B, m, rope, norm;
-    double eps;
+    float eps;
     RowQuant o;
 };
 
 // One listed entry per row: its position is the block end (i + 1) m - 1.
 template <class T, int LPR, bool FP4>
 __global__ void __launch_bounds__(32 * kWarps) indexer_append_kernel(const AppendArgs a, const RopeTable rt) {
+    __shared__ double2 rot64[32 * kWarps][4];
     pdl_wait();
     const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
-    constexpr int kRows = 32 / LPR, D = 8 * LPR;
+    constexpr int kRows = 32 / LPR;
     const int64_t it = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kRows + sub;
     bool in = it < a.n;
     int64_t dst = 0, pos = 0;
@@ -338,26 +497,29 @@ __global__ void __launch_bounds__(32 * kWarps) indexer_append_kernel(const Appen
         if (!ok) {
             if (l == 0) flag(a.o.st, CSA_DEV_OOB);
             in = false;
+            pos = 0;
             r.zero();
         }
     }
-    float w[8], x[8];
-    load_weight<T>(a.weight, 8 * l, w);
-    const bool rot = 8 * l >= D - a.rope;
-    double cs[4], sn[4];
-    if (rot) {
-#pragma unroll
-        for (int p = 0; p < 4; p++) rotation((double)pos, rt.freq[4 * l + p - (D - a.rope) / 2], cs[p], sn[p]);
-    }
+    float w[8], x[8], cs[4], sn[4];
+    load_weight8(a.weight, 8 * l, w);
+    const double2* rot = lane_rotation<LPR>((double)pos, rt, l, a.rope, rot64[threadIdx.x], cs, sn);
     r.get(x);
     quantize_row<LPR, FP4>(x, l, cs, sn, rot, w, a.norm, a.eps, a.o, dst, in);
     __threadfence();
 }
 
-// theta^(-2j / rope) for the pairs j of the rotated channels.
-RopeTable rope_table(int rope, double theta) {
-    RopeTable t = {};
-    for (int j = 0; j < rope / 2; j++) t.freq[j] = pow(theta, -2.0 * j / rope);
+// theta^(-2j / rope) for the pairs j of the rotated channels.  A thread keeps its last table:
+// its 32 powers took 1.0 us of a call's 4.
+const RopeTable& rope_table(int rope, double theta) {
+    static thread_local RopeTable t = {};
+    static thread_local int last_rope = -1;
+    static thread_local double last_theta = 0.0;
+    if (rope != last_rope || theta != last_theta) {
+        for (int j = 0; j < rope / 2; j++) t.freq[j] = pow(theta, -2.0 * j / rope);
+        last_rope = rope;
+        last_theta = theta;
+    }
     return t;
 }
 
@@ -385,7 +547,7 @@ unsigned blocks_of(int64_t tasks) { return (unsigned)((tasks + kWarps - 1) / kWa
 
 template <class T, int LPR, int C>
 cudaError_t run_qk(QkArgs a, const RopeTable& rt, cudaStream_t stream) {
-    split_heads(a.T, a.H + a.Hk, 32 / LPR, a.heads_per_warp, a.warps_per_token);
+    split_heads(a.T, a.q.heads + a.k.heads, 32 / LPR, a.heads_per_warp, a.warps_per_token);
     LaunchScope scope(kKQkNormRope, stream);
     return launch_pdl(qk_norm_rope_kernel<T, LPR, C>, dim3(blocks_of((int64_t)a.T * a.warps_per_token)),
                       dim3(32 * kWarps), 0, stream, a, rt);
@@ -424,9 +586,8 @@ cudaError_t run_append(const AppendArgs& a, const RopeTable& rt, cudaStream_t st
 cudaError_t launch_qk_norm_rope(const QkRows& q, const QkRows& k, const int32_t* pos, int dtype, int T,
                                 int D, int rope, int norm, float theta, float eps,
                                 cudaStream_t stream) {
-    QkArgs a{q.x, k.x, q.out, k.out, q.weight, k.weight, pos, q.st, q.sh, k.st, k.sh, q.ost, q.osh,
-             k.ost, k.osh, T, q.heads, k.heads, D, rope, norm, 0, 0, eps};
-    const RopeTable rt = rope_table(rope, theta);
+    const QkArgs a{q, k, pos, T, D, rope, norm, 0, 0, eps};
+    const RopeTable& rt = rope_table(rope, theta);
     switch (dtype) {
         case CSA_DT_BF16: return run_qk_dims<__nv_bfloat16>(a, rt, stream);
         case CSA_DT_F16: return run_qk_dims<__half>(a, rt, stream);
@@ -455,9 +616,9 @@ cudaError_t launch_indexer_queries(const void* q, int dtype, int64_t st, int64_t
                                    const float* weight, int norm, int rope, float theta, float eps,
                                    int Q, int H, int D, int fmt, uint8_t* codes, void* scale,
                                    int32_t* dev_status, cudaStream_t stream) {
-    QueryArgs a{q, weight, pos, st, sh, Q, H, rope, norm, 0, 0, (double)eps,
+    QueryArgs a{q, weight, pos, st, sh, Q, H, rope, norm, 0, 0, eps,
                 RowQuant{codes, (float*)scale, (uint8_t*)scale, dev_status}};
-    const RopeTable rt = rope_table(rope, theta);
+    const RopeTable& rt = rope_table(rope, theta);
     CSA_ROWS_DISPATCH(run_queries, a);
 }
 
@@ -468,8 +629,8 @@ cudaError_t launch_indexer_append(const void* k, int dtype, int64_t ld, const in
                                   int D, int fmt, uint8_t* codes, void* scale, int32_t* dev_status,
                                   cudaStream_t stream) {
     AppendArgs a{k, weight, ld, seq_len, er, item_seq, item_ent, n, ent_rows, B, m, rope, norm,
-                 (double)eps, RowQuant{codes, (float*)scale, (uint8_t*)scale, dev_status}};
-    const RopeTable rt = rope_table(rope, theta);
+                 eps, RowQuant{codes, (float*)scale, (uint8_t*)scale, dev_status}};
+    const RopeTable& rt = rope_table(rope, theta);
     CSA_ROWS_DISPATCH(run_append, a);
 }
 

@@ -2,8 +2,8 @@
 states through the MXFP4 query projection, the heads' norm, rotation and quantisation; keys
 appended to the hybrid cache's blocks; selection and attention on what they wrote.
 
-Codes are compared bit for bit with the 64-bit forms, and the index sets and outputs with the same
-selection and attention on the 64-bit forms' codes in a contiguous store.  The
+Codes are compared bit for bit with the 64-bit forms, and the index sets with the same selection
+from a contiguous store.  The
 projection's inputs keep fp32 sums exact (K = 256 and block exponents within a few binades:
 multiples of 2^-6 below 2^14), so nothing between the hidden states and the codes rounds twice."""
 import numpy as np
@@ -47,6 +47,12 @@ def _select(fmt, qI, qs, w, kI, ks, seq_len, off, q_seq, q_pos, idx, max_n):
        k=TOPK, max_n=max_n)
 
 
+def _same_scales(got, ref):
+    """Scale bytes exactly, fp32 scales to their 30 roundings of 2^-24 (see test_gpu_inputs)."""
+    got = got.cpu().numpy()
+    assert np.array_equal(got, ref) if ref.dtype == np.uint8 else np.all(np.abs(got - ref) <= 30 * 2.0 ** -24 * ref)
+
+
 def _up(a):
     return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
 
@@ -66,8 +72,15 @@ def test_decode_steps_match_the_64_bit_forms(fmt):
     kv_off = np.concatenate([[0], np.cumsum(Tmax)[:-1]]).astype(np.int64)
     bias = torch.randn((8, D), generator=g, device=DEV) * 0.1
     sink = torch.randn(H, generator=g, device=DEV)
-    kI_ref, ks_ref = _keys_ref(keys, np.concatenate([np.arange(n) for n in n_max]), key_w, fmt)
-    kI_lin, ks_lin = _up(kI_ref), _up(ks_ref)
+    # a contiguous store of every key the run will use; the codes are the 64-bit forms'
+    ient = np.concatenate([np.arange(n) for n in n_max]).astype(np.int32)
+    kI_ref, ks_ref = _keys_ref(keys, ient, key_w, fmt)
+    kI_lin, ks_lin = torch.zeros_like(_up(kI_ref)), torch.zeros_like(_up(ks_ref))
+    L.csa_indexer_append(keys, torch.tensor(Tmax, device=DEV), _up(off),
+                         _up(np.repeat(np.arange(B, dtype=np.int32), n_max)), _up(ient), kI_lin, ks_lin, B=B,
+                         fmt=fmt, weight=key_w)
+    assert np.array_equal(kI_lin.cpu().numpy(), kI_ref)
+    _same_scales(ks_lin, ks_ref)
 
     proj = pipeline.QueryProjection(proj_w, HI, DI, max_q=8, fmt=fmt, head_weight=head_w)
     hc = cache.HybridCache(B, D, 0, DI, n_blocks=40, max_blocks=12, device=DEV, idx_fmt=fmt)
@@ -106,10 +119,11 @@ def test_decode_steps_match_the_64_bit_forms(fmt):
         torch.cuda.synchronize()
         assert int(hc.dev_status.item()) == 0 and int(proj.dev_status.item()) == 0, s
         ref = _heads_ref(x, proj_w, q_pos, head_w, fmt)
-        assert np.array_equal(qI.cpu().numpy(), ref[0]) and np.array_equal(qs.cpu().numpy(), ref[1]), s
-        # the same selection from a contiguous store of the 64-bit forms' codes
+        assert np.array_equal(qI.cpu().numpy(), ref[0]), s
+        _same_scales(qs, ref[1])
+        # the same selection from the contiguous store
         idx_ref = torch.full_like(idx, -1)
-        _select(fmt, _up(ref[0]), _up(ref[1]), w, kI_lin, ks_lin, torch.tensor([t + 1 for t in p], device=DEV),
+        _select(fmt, _up(ref[0]), qs.clone(), w, kI_lin, ks_lin, torch.tensor([t + 1 for t in p], device=DEV),
                 _up(off), q_seq, q_pos, idx_ref, max(t + 1 for t in p) // 4)
         assert torch.equal(idx, idx_ref), s
         assert bool(out.isfinite().all())
