@@ -170,21 +170,27 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const QkArgs 
 // (or a block's power-of-two scale) next to a rounding border is not left to fp32.  The fast
 // path computes in fp32 and brackets every quotient z by its error bound: if the codes of z -
 // margin and z + margin agree, that code is the one.  If they differ anywhere in the warp's
-// rows (about 1 pass in 300 for MXFP4, 1 in 80 for e4m3, on normal data), or the values
-// leave the range the bound holds in, the rows are done again in fp64.
+// rows (about 1 pass in 60 on normal data), or the values leave the range the bound holds in,
+// the rows are done again in fp64.
 //
-// The bound, u = 2^-24, relative to |y| (|y1| + |y2| in a rotated pair): the sum of squares
-// takes at most 5 roundings in a lane and log2(LPR) <= 4 across, with eps 10 u, of which rsqrt
-// halves 5 u and adds its 2 ulp = 4 u; the products with weight and x add 2 u, cos and sin u,
-// the rotation's product, sum and the rounding of its result 3 u: 15 u.  The bracket's
-// own rounding adds u: 16 u < kFp4Margin.  The e4m3 quotient is y * (448 / max|y|), in which r
-// cancels: 6 u of y, twice 6 u of the largest |y| (|y1| + |y2| <= 2 max), 2 u of the quotient
-// and the product, 1 u of the bracket: 21 u < kFp8Margin.  In both, |z| is at most the
-// bracketed magnitude.  Between 2^-60 and 2^120 an underflowed product is below 2^-34 of a
-// quotient's unit, far from every border but zero's, whose sign it keeps.
+// v = x * weight, rotated, is left without the norm's factor r, which joins the scale.  The
+// bound, u = 2^-24, relative to |v1| + |v2| of a rotated pair before the rotation (|v|
+// elsewhere): the product with the weight, cos or sin, the product with it, the sum: 4 u.
+//   MXFP4: z = v * (r * 2^-e).  The sum of squares takes at most 5 roundings in a lane and
+//   log2(LPR) <= 4 across, the mean and eps 1, of which rsqrt halves 5 u and adds its
+//   2 ulp = 4 u; the product u, the bracket u: 15 u of |v1| + |v2| <= 2 max|v| (a rotation
+//   keeps the pair's length).  The bracket is one margin per block, 2 max|z| kFp4Margin.
+//   e4m3: z = v * (448 / max|v|), from which r drops out: 4 u, twice 4 u of the largest |v|, u
+//   each of the division, the product, the definition's rounding of the scale to fp32 and the
+//   bracket: 16 u.  The bracket is relative to each element, since the codes near zero are dense.
+// With rows' sums of squares below 2^100, weights below 2^40 and results within 2^-60 .. 2^100
+// nothing overflows, and an underflowed product is below 2^-34 of a quotient's unit, far from
+// every border but zero's, whose sign it keeps.  (An exact zero beside other values always
+// takes the fp64 path of MXFP4, where its bracket has both signs.)
 constexpr float kU24 = 5.9604645e-08f;
 constexpr float kFp4Margin = 20.f * kU24;
-constexpr float kFp8Margin = 24.f * kU24;
+constexpr float kFp8Margin = 20.f * kU24;
+constexpr float kTiny = 8.6736174e-19f, kHuge = 1.2676506e+30f;   // 2^-60, 2^100
 
 struct RowQuant {
     uint8_t* codes;    // rows of D (e4m3) or D / 2 (e2m1) bytes
@@ -282,83 +288,93 @@ __device__ __noinline__ RowCodes quantize_row_f64(const Eight x, const Eight w, 
 
 // One row over LPR = D / 8 lanes (all lanes of the warp call it): norm, rotation (cs, sn of
 // this lane's 4 pairs where rot is given, rot the same in fp64), codes and scale to row `dst`.
+// near: whether this lane's weights are past the fast path's range.
 template <int LPR, bool FP4>
 __device__ __forceinline__ void quantize_row(const float* x, int l, const float* cs, const float* sn,
-                                             const double2* rot, const float* w, bool norm, float eps,
+                                             const double2* rot, const float* w, bool near, bool norm, float eps,
                                              const RowQuant& o, int64_t dst, bool in) {
     constexpr int D = 8 * LPR;
-    float r = 1.f;
-    bool near = false;          // not settled in fp32
-    if (norm) {
-        float s0 = 0.f, s1 = 0.f;
+    float s[2] = {0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            s0 = fmaf(x[j], x[j], s0);
-            s1 = fmaf(x[j + 1], x[j + 1], s1);
-        }
-        const float ms = fmaf(group_sum<LPR>(s0 + s1), 1.f / D, eps);
-        near = !(ms > 8.6736174e-19f && ms < 1.2676506e+30f);    // 2^-60, 2^100
+    for (int j = 0; j < 8; j += 2) fma2(s, x + j, x + j, s);
+    const float ss = group_sum<LPR>(s[0] + s[1]);     // a NaN or infinity of the row shows here
+    near |= !(ss < kHuge);
+    float r = 1.f;
+    if (norm) {
+        const float ms = fmaf(ss, 1.f / D, eps);
+        near |= !(ms > kTiny);
         r = rsqrtf(ms);
     }
-    float y[8], mag[8];
+    float v[8], mag[8];
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-        y[j] = x[j] * (r * w[j]);
-        mag[j] = fabsf(y[j]);
+    for (int j = 0; j < 8; j += 2) mul2(v + j, x + j, w + j);
+    if constexpr (!FP4) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) mag[j] = fabsf(v[j]);
     }
     if (rot) {
 #pragma unroll
         for (int p = 0; p < 4; p++) {
-            const float a = y[2 * p], b = y[2 * p + 1];
-            mag[2 * p] = mag[2 * p + 1] = fabsf(a) + fabsf(b);
-            y[2 * p] = fmaf(a, cs[p], -(b * sn[p]));
-            y[2 * p + 1] = fmaf(a, sn[p], b * cs[p]);
+            const float a = v[2 * p], b = v[2 * p + 1];
+            if constexpr (!FP4) mag[2 * p] = mag[2 * p + 1] = fabsf(a) + fabsf(b);
+            v[2 * p] = fmaf(a, cs[p], -(b * sn[p]));
+            v[2 * p + 1] = fmaf(a, sn[p], b * cs[p]);
         }
     }
-    uint32_t top = 0;           // as bits: a NaN is above all
+    float amax = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; j++) top = max(top, __float_as_uint(y[j]) & 0x7fffffffu);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    for (int j = 0; j < 8; j++) amax = fmaxf(amax, fabsf(v[j]));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     if constexpr (!FP4) {
 #pragma unroll
-        for (int s = 4; s < LPR; s <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
+        for (int m = 4; m < LPR; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
     }
-    const float amax = __uint_as_float(top);
-    // 2^-60 .. 2^120, or a block of zeros
-    near |= top != 0u && !(amax > 8.6736174e-19f && amax < 1.3292280e+36f);
+    const bool zero = amax == 0.f;
+    near |= !zero && !(amax > kTiny);
     RowCodes c;
     c.bad = false;
-    float inv, margin;
-    if constexpr (FP4) {
-        const uint32_t ex = top >> 23, e = ex > 2u ? ex - 2u : 0u;
-        // the largest magnitude may itself lie next to a power of two (|y1| + |y2| <= 2 amax)
-        near |= __float_as_uint(fmaf(amax, 2.1f * kFp4Margin, amax)) >> 23 != ex ||
-                __float_as_uint(fmaf(amax, -2.1f * kFp4Margin, amax)) >> 23 != ex;
-        inv = __uint_as_float((254u - min(e, 253u)) << 23);      // 2^(127 - e)
-        margin = kFp4Margin * inv;
-        c.scale = e;
-    } else {
-        inv = top ? 448.f / amax : 1.f;
-        margin = kFp8Margin * inv;
-        c.scale = __float_as_uint(top ? amax * (1.f / 448.f) : 1.f);
-    }
     float lo[8], hi[8];
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        const float z = y[j] * inv;
-        lo[j] = fmaf(-mag[j], margin, z);
-        hi[j] = fmaf(mag[j], margin, z);
-    }
     if constexpr (FP4) {
+        const float top = amax * r;
+        const uint32_t ex = __float_as_uint(top) >> 23;
+        // the largest magnitude may itself lie next to a power of two
+        near |= !zero && (!(top > kTiny && top < kHuge) ||
+                          __float_as_uint(fmaf(top, 2.1f * kFp4Margin, top)) >> 23 != ex ||
+                          __float_as_uint(fmaf(top, -2.1f * kFp4Margin, top)) >> 23 != ex);
+        // a non-finite block is `near`: the minimum only keeps the shift in range
+        const uint32_t e = zero ? 0u : max(min(ex, 250u), 2u) - 2u;
+        c.scale = e;
+        const float inv = zero ? 1.f : r * __uint_as_float((254u - e) << 23);     // r * 2^(127 - e)
+        const float inv2[2] = {inv, inv};
+        const float m = 2.f * kFp4Margin * (amax * inv), up[2] = {m, m}, down[2] = {-m, -m};
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            float z[2];
+            mul2(z, v + j, inv2);
+            add2(lo + j, z, down);
+            add2(hi + j, z, up);
+        }
         c.c0 = pack_e2m1x8(lo);
         c.c1 = 0;
-        near |= pack_e2m1x8(hi) != c.c0;
+        near |= !zero && pack_e2m1x8(hi) != c.c0;     // zeros keep their sign in lo
     } else {
+        const float inv = zero ? 1.f : 448.f / amax;
+        const float inv2[2] = {inv, inv};
+        const float m = kFp8Margin * inv, up[2] = {m, m}, down[2] = {-m, -m};
+        c.scale = __float_as_uint(zero ? 1.f : (amax * r) * (1.f / 448.f));
+        near |= !zero && !(amax * r > kTiny && amax * r < kHuge);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            float z[2];
+            mul2(z, v + j, inv2);
+            fma2(lo + j, mag + j, down, z);
+            fma2(hi + j, mag + j, up, z);
+        }
         const uint2 a = pack_e4m3x8(lo), b = pack_e4m3x8(hi);
         c.c0 = a.x;
         c.c1 = a.y;
-        near |= a.x != b.x || a.y != b.y;
+        near |= !zero && (a.x != b.x || a.y != b.y);
     }
     if (__any_sync(0xffffffffu, near)) {
         Eight xv, wv;
@@ -383,6 +399,14 @@ __device__ __forceinline__ void quantize_row(const float* x, int l, const float*
             if (c.bad) flag(o.st, CSA_DEV_NAN);
         }
     }
+}
+
+// Whether a weight is not finite or past what the fast path's bound holds for.
+__device__ __forceinline__ bool weight_past_range(const float* w) {
+    bool past = false;
+#pragma unroll
+    for (int j = 0; j < 8; j++) past |= !(fabsf(w[j]) < 1.0995116e+12f);   // 2^40
+    return past;
 }
 
 // This lane's 4 rotation pairs: fp32 in registers, fp64 in shared memory for the fp64 path
@@ -432,6 +456,7 @@ __global__ void __launch_bounds__(32 * kWarps) indexer_queries_kernel(const Quer
     const int h1 = min(h0 + a.heads_per_warp, a.H);
     float w[8], cs[4], sn[4];
     load_weight8(a.weight, 8 * l, w);
+    const bool past = weight_past_range(w);
     const T* src = (const T*)a.q + t * a.st + (h0 + sub) * a.sh + 8 * l;
     constexpr int kU = 2;                // rows a lane loads ahead of the one it works on
     Row8<T> r[kU];
@@ -451,7 +476,7 @@ __global__ void __launch_bounds__(32 * kWarps) indexer_queries_kernel(const Quer
         r[kU - 1].zero();
         src += kRows * a.sh;
         if (h + kU * kRows < h1) r[kU - 1].load(src + (kU - 1) * kRows * a.sh);
-        quantize_row<LPR, FP4>(x, l, cs, sn, rot, w, a.norm, a.eps, a.o, dst, h < h1);
+        quantize_row<LPR, FP4>(x, l, cs, sn, rot, w, past, a.norm, a.eps, a.o, dst, h < h1);
         dst += kRows;
     }
     __threadfence();
@@ -505,7 +530,7 @@ __global__ void __launch_bounds__(32 * kWarps) indexer_append_kernel(const Appen
     load_weight8(a.weight, 8 * l, w);
     const double2* rot = lane_rotation<LPR>((double)pos, rt, l, a.rope, rot64[threadIdx.x], cs, sn);
     r.get(x);
-    quantize_row<LPR, FP4>(x, l, cs, sn, rot, w, a.norm, a.eps, a.o, dst, in);
+    quantize_row<LPR, FP4>(x, l, cs, sn, rot, w, weight_past_range(w), a.norm, a.eps, a.o, dst, in);
     __threadfence();
 }
 

@@ -131,6 +131,30 @@ __device__ __forceinline__ uint2 pack_e4m3x8(const float* y) {
     return make_uint2(w[0], w[1]);
 }
 
+// Two fp32 operations in one instruction, each rounded as its own.
+__device__ __forceinline__ uint64_t bits2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void mul2(float* d, const float* a, const float* b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a[0], a[1])), "l"(bits2(b[0], b[1])));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d[0]), "=f"(d[1]) : "l"(r));
+}
+__device__ __forceinline__ void add2(float* d, const float* a, const float* b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a[0], a[1])), "l"(bits2(b[0], b[1])));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d[0]), "=f"(d[1]) : "l"(r));
+}
+__device__ __forceinline__ void fma2(float* d, const float* a, const float* b, const float* c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(bits2(a[0], a[1])), "l"(bits2(b[0], b[1])), "l"(bits2(c[0], c[1])));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d[0]), "=f"(d[1]) : "l"(r));
+}
+
 // z as an fp32 whose last bit is set where bits were cut off ("rounded to odd"): rounding the
 // result to a format of at most 21 fraction bits gives what rounding z itself gives.
 // Magnitudes below 2^-126 come back as one just above it (for the formats here both round to

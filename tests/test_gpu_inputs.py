@@ -410,3 +410,35 @@ def test_empty_calls_launch_nothing():
                          torch.empty(4, device=DEV), B=1)
     torch.cuda.synchronize()
     assert L.csa_launch_count() == n0
+
+
+@pytest.mark.parametrize("fmt", [L.CSA_IDX_FP8, L.CSA_IDX_MXFP4])
+@pytest.mark.parametrize("what", ["tiny", "huge", "weights", "zeros", "no eps", "spread", "nan weight"])
+def test_indexer_queries_past_the_fp32_range(what, fmt):
+    # inputs that the fp32 bracket does not cover: settled in fp64, same codes
+    g = torch.Generator(device=DEV).manual_seed(77)
+    x = torch.randn((40, 8, 128), generator=g, device=DEV)
+    w = torch.ones(128, device=DEV)
+    eps = 1e-6
+    if what == "tiny":
+        x *= 1e-25
+    elif what == "huge":
+        x *= 1e17
+    elif what == "weights":
+        w = torch.exp2(torch.randint(-60, 60, (128,), generator=g, device=DEV).float())
+    elif what == "zeros":
+        x[:, :, ::3] = 0
+        x[:, ::2, 32:64] = 0
+    elif what == "no eps":
+        x *= torch.exp2(torch.randint(-45, 45, (40, 8, 1), generator=g, device=DEV).float())
+        eps = 0.0
+    elif what == "spread":
+        x *= torch.exp2(torch.randint(-40, 20, (40, 8, 128), generator=g, device=DEV).float())
+    else:
+        w[5] = float("nan")
+    pos = torch.randint(1, 1 << 20, (40,), generator=g, device=DEV, dtype=torch.int32)
+    codes, scale = _store(fmt, (40, 8), 128)
+    st = _status()
+    L.csa_indexer_queries(x, pos, codes, scale, fmt=fmt, weight=w, eps=eps, dev_status=st)
+    _sync(st, L.CSA_DEV_NAN if what == "nan weight" else 0)
+    _same(codes, scale, _quant_ref(io.norm_rope(f64(x), pos.cpu().numpy(), f64(w), eps=eps), fmt))
