@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const QkArgs 
             }
         }
     }
-    constexpr int kU = C == 1 ? 4 : 1;
+    constexpr int kU = C == 1 ? 4 : C == 2 ? 2 : 1;
     if (h0 < a.q.heads)
         norm_rope_heads<T, LPR, C, kU>(a.q, t, h0, min(h1, a.q.heads), a.D, lo, a.norm, a.eps, sub, l, cs, sn);
     if (h1 > a.q.heads)
@@ -176,8 +176,8 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const QkArgs 
 // v = x * weight, rotated, is left without the norm's factor r, which joins the scale.  The
 // bound, u = 2^-24, relative to |v1| + |v2| of a rotated pair before the rotation (|v|
 // elsewhere): the product with the weight, cos or sin, the product with it, the sum: 4 u.
-//   MXFP4: z = v * (r * 2^-e).  The sum of squares takes at most 5 roundings in a lane and
-//   log2(LPR) <= 4 across, the mean and eps 1, of which rsqrt halves 5 u and adds its
+//   MXFP4: z = v * (r * 2^-e).  The sum of squares takes at most 6 roundings in a lane and
+//   log2(LPR) <= 3 across, the mean and eps 1, of which rsqrt halves 5 u and adds its
 //   2 ulp = 4 u; the product u, the bracket u: 15 u of |v1| + |v2| <= 2 max|v| (a rotation
 //   keeps the pair's length).  The bracket is one margin per block, 2 max|z| kFp4Margin.
 //   e4m3: z = v * (448 / max|v|), from which r drops out: 4 u, twice 4 u of the largest |v|, u
@@ -199,105 +199,134 @@ struct RowQuant {
     int32_t* st;
 };
 
-// A row's result in a lane: its 8 codes (4 bytes for e2m1) and scale, and whether it is bad.
-struct RowCodes {
-    uint32_t c0, c1;
-    uint32_t scale;    // fp32 bits, or the UE8M0 byte
-    bool bad;
+// A row's (or a lane's) values: kC chunks of 8 channels, chunk c of lane l at 8 (l + LPR c).
+constexpr int kC = 2;
+struct Lane {
+    float v[kC][8];
 };
 
-struct Eight {
-    float v[8];
+// Codes of one lane's chunks (e2m1: the first word of each), their scales, what is bad.
+struct RowCodes {
+    uint32_t c[kC][2];
+    uint32_t scale[kC];   // UE8M0 byte per chunk's block, or the row's fp32 bits
+    bool bad[kC];
 };
 
 // The row in fp64 from the input's bits to the codes.  Out of line, its arguments by value: an
 // array whose address is taken would live in local memory on the fast path too.
 template <int LPR, bool FP4>
-__device__ __noinline__ RowCodes quantize_row_f64(const Eight x, const Eight w, const double2* rot, bool norm,
-                                                  double eps) {
-    constexpr int D = 8 * LPR;
-    double y[8];
+__device__ __noinline__ RowCodes quantize_row_f64(const Lane x, const Lane w, const double2* rot0,
+                                                  const double2* rot1, bool norm, double eps) {
+    constexpr int D = 8 * kC * LPR;
+    double y[kC][8];
     double ss = 0.0;
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-        y[j] = (double)x.v[j];
-        ss = fma(y[j], y[j], ss);
-    }
+    for (int c = 0; c < kC; c++)
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            y[c][j] = (double)x.v[c][j];
+            ss = fma(y[c][j], y[c][j], ss);
+        }
     double r = 1.0;
     if (norm) r = rsqrt(group_sum<LPR>(ss) * (1.0 / D) + eps);
 #pragma unroll
-    for (int j = 0; j < 8; j++) y[j] *= r * (double)w.v[j];
-    if (rot) {
+    for (int c = 0; c < kC; c++) {
+        const double2* rot = c ? rot1 : rot0;
 #pragma unroll
-        for (int p = 0; p < 4; p++) {
-            const double2 cs = rot[p];
-            const double a = y[2 * p], b = y[2 * p + 1];
-            y[2 * p] = a * cs.x - b * cs.y;
-            y[2 * p + 1] = a * cs.y + b * cs.x;
+        for (int j = 0; j < 8; j++) y[c][j] *= r * (double)w.v[c][j];
+        if (rot) {
+#pragma unroll
+            for (int p = 0; p < 4; p++) {
+                const double2 cs = rot[p];
+                const double a = y[c][2 * p], b = y[c][2 * p + 1];
+                y[c][2 * p] = a * cs.x - b * cs.y;
+                y[c][2 * p + 1] = a * cs.y + b * cs.x;
+            }
         }
     }
     RowCodes o;
-    float f[8];
     if constexpr (FP4) {
-        // the block's scale needs the exponent of its largest magnitude only
-        int top = 0;
 #pragma unroll
-        for (int j = 0; j < 8; j++) top = max(top, __double2hiint(y[j]) & 0x7fffffff);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int ex = (top >> 20) - 1023;              // floor(log2(amax)); -1023 for zeros
-        o.bad = ex > 129;                               // not finite, or past the scales' range
-        const int e = o.bad ? 255 : max(ex - 2 + 127, 0);
-        const double inv = __hiloint2double((1023 + 127 - (o.bad ? 127 : e)) << 20, 0);
+        for (int c = 0; c < kC; c++) {
+            // the block's scale needs the exponent of its largest magnitude only
+            int top = 0;
 #pragma unroll
-        for (int j = 0; j < 8; j++) f[j] = f64_to_f32_odd(o.bad ? 0.0 : y[j] * inv);
-        o.c0 = pack_e2m1x8(f);
-        o.c1 = 0;
-        o.scale = (uint32_t)e;
+            for (int j = 0; j < 8; j++) top = max(top, __double2hiint(y[c][j]) & 0x7fffffff);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int ex = (top >> 20) - 1023;              // floor(log2(amax)); -1023 for zeros
+            const bool bad = ex > 129;                      // not finite, or past the scales' range
+            const int e = bad ? 255 : max(ex - 2 + 127, 0);
+            const double inv = __hiloint2double((1023 + 127 - (bad ? 127 : e)) << 20, 0);
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) f[j] = f64_to_f32_odd(bad ? 0.0 : y[c][j] * inv);
+            o.c[c][0] = pack_e2m1x8(f);
+            o.c[c][1] = 0;
+            o.scale[c] = (uint32_t)e;
+            o.bad[c] = bad;
+        }
     } else {
         double top = 0.0;
         bool nan = false;
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            top = fmax(top, fabs(y[j]));
-            nan |= y[j] != y[j];
-        }
+        for (int c = 0; c < kC; c++)
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                top = fmax(top, fabs(y[c][j]));
+                nan |= y[c][j] != y[c][j];
+            }
 #pragma unroll
         for (int s = LPR / 2; s > 0; s >>= 1) {
             top = fmax(top, __shfl_xor_sync(0xffffffffu, top, s));
             nan |= __shfl_xor_sync(0xffffffffu, (int)nan, s) != 0;
         }
         float scale = (float)(top / 448.0);
-        o.bad = nan || !(scale <= 3.402823466e38f);
-        if (!(scale > 0.f) || o.bad) scale = 1.f;
+        const bool bad = nan || !(scale <= 3.402823466e38f);
+        if (!(scale > 0.f) || bad) scale = 1.f;
         // y / scale: the product with the rounded reciprocal, mended once by its remainder, so
         // that a quotient fp64 holds (a tie between two codes, say) comes out exactly
         const double sd = (double)scale, inv = 1.0 / sd;
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const double z = y[j] * inv;
-            f[j] = f64_to_f32_odd(o.bad ? 0.0 : fma(fma(-z, sd, y[j]), inv, z));
+        for (int c = 0; c < kC; c++) {
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const double z = y[c][j] * inv;
+                f[j] = f64_to_f32_odd(bad ? 0.0 : fma(fma(-z, sd, y[c][j]), inv, z));
+            }
+            const uint2 q = pack_e4m3x8(f);
+            o.c[c][0] = q.x;
+            o.c[c][1] = q.y;
+            o.scale[c] = bad ? 0x7fffffffu : __float_as_uint(scale);
+            o.bad[c] = bad;
         }
-        const uint2 c = pack_e4m3x8(f);
-        o.c0 = c.x;
-        o.c1 = c.y;
-        o.scale = o.bad ? 0x7fffffffu : __float_as_uint(scale);
     }
     return o;
 }
 
-// One row over LPR = D / 8 lanes (all lanes of the warp call it): norm, rotation (cs, sn of
-// this lane's 4 pairs where rot is given, rot the same in fp64), codes and scale to row `dst`.
-// near: whether this lane's weights are past the fast path's range.
+// What a lane keeps for the rows of one position: weights, its pairs' cosines and sines (fp32;
+// fp64 in shared memory, null for a chunk that is not rotated).
+struct LaneParams {
+    Lane w;
+    float cs[kC][4], sn[kC][4];
+    const double2* rot[kC];
+    bool past;         // a weight the fast path's bound does not hold for
+};
+
+// One row over LPR = D / 16 lanes (all lanes of the warp call it): norm, rotation, codes and
+// scale to row `dst`.
 template <int LPR, bool FP4>
-__device__ __forceinline__ void quantize_row(const float* x, int l, const float* cs, const float* sn,
-                                             const double2* rot, const float* w, bool near, bool norm, float eps,
+__device__ __forceinline__ void quantize_row(const Lane& x, int l, const LaneParams& p, bool norm, float eps,
                                              const RowQuant& o, int64_t dst, bool in) {
-    constexpr int D = 8 * LPR;
-    float s[2] = {0.f, 0.f};
+    constexpr int D = 8 * kC * LPR;
+    bool near = p.past;         // not settled in fp32
+    float s[kC][2] = {};
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) fma2(s, x + j, x + j, s);
-    const float ss = group_sum<LPR>(s[0] + s[1]);     // a NaN or infinity of the row shows here
+    for (int c = 0; c < kC; c++)
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) fma2(s[c], x.v[c] + j, x.v[c] + j, s[c]);
+    const float ss = group_sum<LPR>((s[0][0] + s[0][1]) + (s[1][0] + s[1][1]));   // NaNs and infinities show here
     near |= !(ss < kHuge);
     float r = 1.f;
     if (norm) {
@@ -305,132 +334,160 @@ __device__ __forceinline__ void quantize_row(const float* x, int l, const float*
         near |= !(ms > kTiny);
         r = rsqrtf(ms);
     }
-    float v[8], mag[8];
+    Lane v, mag;
+    float amax[kC];
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) mul2(v + j, x + j, w + j);
-    if constexpr (!FP4) {
+    for (int c = 0; c < kC; c++) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) mag[j] = fabsf(v[j]);
-    }
-    if (rot) {
+        for (int j = 0; j < 8; j += 2) mul2(v.v[c] + j, x.v[c] + j, p.w.v[c] + j);
+        if constexpr (!FP4) {
 #pragma unroll
-        for (int p = 0; p < 4; p++) {
-            const float a = v[2 * p], b = v[2 * p + 1];
-            if constexpr (!FP4) mag[2 * p] = mag[2 * p + 1] = fabsf(a) + fabsf(b);
-            v[2 * p] = fmaf(a, cs[p], -(b * sn[p]));
-            v[2 * p + 1] = fmaf(a, sn[p], b * cs[p]);
+            for (int j = 0; j < 8; j++) mag.v[c][j] = fabsf(v.v[c][j]);
         }
-    }
-    float amax = 0.f;
+        if (p.rot[c]) {
 #pragma unroll
-    for (int j = 0; j < 8; j++) amax = fmaxf(amax, fabsf(v[j]));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    if constexpr (!FP4) {
+            for (int i = 0; i < 4; i++) {
+                const float a = v.v[c][2 * i], b = v.v[c][2 * i + 1];
+                if constexpr (!FP4) mag.v[c][2 * i] = mag.v[c][2 * i + 1] = fabsf(a) + fabsf(b);
+                v.v[c][2 * i] = fmaf(a, p.cs[c][i], -(b * p.sn[c][i]));
+                v.v[c][2 * i + 1] = fmaf(a, p.sn[c][i], b * p.cs[c][i]);
+            }
+        }
+        amax[c] = 0.f;
 #pragma unroll
-        for (int m = 4; m < LPR; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+        for (int j = 0; j < 8; j++) amax[c] = fmaxf(amax[c], fabsf(v.v[c][j]));
     }
-    const bool zero = amax == 0.f;
-    near |= !zero && !(amax > kTiny);
-    RowCodes c;
-    c.bad = false;
-    float lo[8], hi[8];
+    RowCodes q;
     if constexpr (FP4) {
-        const float top = amax * r;
-        const uint32_t ex = __float_as_uint(top) >> 23;
-        // the largest magnitude may itself lie next to a power of two
-        near |= !zero && (!(top > kTiny && top < kHuge) ||
-                          __float_as_uint(fmaf(top, 2.1f * kFp4Margin, top)) >> 23 != ex ||
-                          __float_as_uint(fmaf(top, -2.1f * kFp4Margin, top)) >> 23 != ex);
-        // a non-finite block is `near`: the minimum only keeps the shift in range
-        const uint32_t e = zero ? 0u : max(min(ex, 250u), 2u) - 2u;
-        c.scale = e;
-        const float inv = zero ? 1.f : r * __uint_as_float((254u - e) << 23);     // r * 2^(127 - e)
-        const float inv2[2] = {inv, inv};
-        const float m = 2.f * kFp4Margin * (amax * inv), up[2] = {m, m}, down[2] = {-m, -m};
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            float z[2];
-            mul2(z, v + j, inv2);
-            add2(lo + j, z, down);
-            add2(hi + j, z, up);
+        for (int c = 0; c < kC; c++) {
+            amax[c] = fmaxf(amax[c], __shfl_xor_sync(0xffffffffu, amax[c], 1));
+            amax[c] = fmaxf(amax[c], __shfl_xor_sync(0xffffffffu, amax[c], 2));
+            const bool zero = amax[c] == 0.f;
+            const float top = amax[c] * r;
+            const uint32_t ex = __float_as_uint(top) >> 23;
+            // the largest magnitude may itself lie next to a power of two
+            near |= !zero && (!(amax[c] > kTiny) || !(top > kTiny && top < kHuge) ||
+                              __float_as_uint(fmaf(top, 2.1f * kFp4Margin, top)) >> 23 != ex ||
+                              __float_as_uint(fmaf(top, -2.1f * kFp4Margin, top)) >> 23 != ex);
+            // a non-finite block is `near`: the bounds only keep the shift in range
+            const uint32_t e = zero ? 0u : max(min(ex, 250u), 2u) - 2u;
+            q.scale[c] = e;
+            q.bad[c] = false;
+            const float inv = zero ? 1.f : r * __uint_as_float((254u - e) << 23);     // r * 2^(127 - e)
+            const float inv2[2] = {inv, inv};
+            const float m = 2.f * kFp4Margin * (amax[c] * inv), up[2] = {m, m}, down[2] = {-m, -m};
+            float lo[8], hi[8];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                float z[2];
+                mul2(z, v.v[c] + j, inv2);
+                add2(lo + j, z, down);
+                add2(hi + j, z, up);
+            }
+            q.c[c][0] = pack_e2m1x8(lo);
+            q.c[c][1] = 0;
+            near |= !zero && pack_e2m1x8(hi) != q.c[c][0];     // zeros keep their sign in lo
         }
-        c.c0 = pack_e2m1x8(lo);
-        c.c1 = 0;
-        near |= !zero && pack_e2m1x8(hi) != c.c0;     // zeros keep their sign in lo
     } else {
-        const float inv = zero ? 1.f : 448.f / amax;
+        float top = fmaxf(amax[0], amax[1]);
+#pragma unroll
+        for (int m = 1; m < LPR; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+        const bool zero = top == 0.f;
+        near |= !zero && !(top > kTiny && top * r > kTiny && top * r < kHuge);
+        const float inv = zero ? 1.f : 448.f / top;
         const float inv2[2] = {inv, inv};
         const float m = kFp8Margin * inv, up[2] = {m, m}, down[2] = {-m, -m};
-        c.scale = __float_as_uint(zero ? 1.f : (amax * r) * (1.f / 448.f));
-        near |= !zero && !(amax * r > kTiny && amax * r < kHuge);
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            float z[2];
-            mul2(z, v + j, inv2);
-            fma2(lo + j, mag + j, down, z);
-            fma2(hi + j, mag + j, up, z);
+        for (int c = 0; c < kC; c++) {
+            float lo[8], hi[8];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                float z[2];
+                mul2(z, v.v[c] + j, inv2);
+                fma2(lo + j, mag.v[c] + j, down, z);
+                fma2(hi + j, mag.v[c] + j, up, z);
+            }
+            const uint2 a = pack_e4m3x8(lo), b = pack_e4m3x8(hi);
+            q.c[c][0] = a.x;
+            q.c[c][1] = a.y;
+            q.scale[c] = __float_as_uint(zero ? 1.f : (top * r) * (1.f / 448.f));
+            q.bad[c] = false;
+            near |= !zero && (a.x != b.x || a.y != b.y);
         }
-        const uint2 a = pack_e4m3x8(lo), b = pack_e4m3x8(hi);
-        c.c0 = a.x;
-        c.c1 = a.y;
-        near |= !zero && (a.x != b.x || a.y != b.y);
     }
-    if (__any_sync(0xffffffffu, near)) {
-        Eight xv, wv;
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-            xv.v[j] = x[j];
-            wv.v[j] = w[j];
-        }
-        c = quantize_row_f64<LPR, FP4>(xv, wv, rot, norm, (double)eps);
+    const unsigned unsettled = __ballot_sync(0xffffffffu, near);
+    if (unsettled) {
+        const RowCodes d = quantize_row_f64<LPR, FP4>(x, p.w, p.rot[0], p.rot[1], norm, (double)eps);
+        // by row: the fp32 scale of a settled neighbour may differ from the fp64 one in its
+        // last bits, and a row's result must not depend on the rows beside it
+        if (unsettled >> ((threadIdx.x & 31) & ~(LPR - 1)) & ((1u << LPR) - 1u)) q = d;
     }
     if (!in) return;
     if constexpr (FP4) {
-        reinterpret_cast<uint32_t*>(o.codes)[dst * (D / 8) + l] = c.c0;
-        if ((l & 3) == 0) {
-            o.sf[dst * (D / 32) + (l >> 2)] = (uint8_t)c.scale;
-            if (c.bad) flag(o.st, CSA_DEV_NAN);
+        uint32_t* codes = reinterpret_cast<uint32_t*>(o.codes) + dst * (D / 8) + l;
+        uint8_t* sf = o.sf + dst * (D / 32) + (l >> 2);
+#pragma unroll
+        for (int c = 0; c < kC; c++) {
+            codes[LPR * c] = q.c[c][0];
+            if ((l & 3) == 0) {
+                sf[LPR / 4 * c] = (uint8_t)q.scale[c];
+                if (q.bad[c]) flag(o.st, CSA_DEV_NAN);
+            }
         }
     } else {
-        reinterpret_cast<uint2*>(o.codes)[dst * LPR + l] = make_uint2(c.c0, c.c1);
+        uint2* codes = reinterpret_cast<uint2*>(o.codes) + dst * (D / 8) + l;
+#pragma unroll
+        for (int c = 0; c < kC; c++) codes[LPR * c] = make_uint2(q.c[c][0], q.c[c][1]);
         if (l == 0) {
-            o.scale[dst] = __uint_as_float(c.scale);
-            if (c.bad) flag(o.st, CSA_DEV_NAN);
+            o.scale[dst] = __uint_as_float(q.scale[0]);
+            if (q.bad[0]) flag(o.st, CSA_DEV_NAN);
         }
     }
 }
 
-// Whether a weight is not finite or past what the fast path's bound holds for.
-__device__ __forceinline__ bool weight_past_range(const float* w) {
-    bool past = false;
+// The lane's weights and its pairs' rotation at `pos`; mine: its fp64 cosines and sines.
+template <int LPR>
+__device__ __forceinline__ void lane_params(LaneParams& p, const float* weight, double pos, const RopeTable& rt,
+                                            int l, int rope, double2* mine) {
+    p.past = false;
 #pragma unroll
-    for (int j = 0; j < 8; j++) past |= !(fabsf(w[j]) < 1.0995116e+12f);   // 2^40
-    return past;
+    for (int c = 0; c < kC; c++) {
+        load_weight8(weight, 8 * (l + LPR * c), p.w.v[c]);
+#pragma unroll
+        for (int j = 0; j < 8; j++) p.past |= !(fabsf(p.w.v[c][j]) < 1.0995116e+12f);   // 2^40, or a NaN
+        const int first = 4 * (l + LPR * c) - (8 * kC * LPR - rope) / 2;
+        p.rot[c] = first < 0 ? nullptr : mine + 4 * c;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            p.cs[c][i] = 1.f;
+            p.sn[c][i] = 0.f;
+            if (first >= 0) {
+                double cd, sd;
+                rotation(pos, rt.freq[first + i], cd, sd);
+                mine[4 * c + i] = make_double2(cd, sd);
+                p.cs[c][i] = (float)cd;
+                p.sn[c][i] = (float)sd;
+            }
+        }
+    }
 }
 
-// This lane's 4 rotation pairs: fp32 in registers, fp64 in shared memory for the fp64 path
-// (nullptr where the lane's channels are not rotated).
-template <int LPR>
-__device__ __forceinline__ const double2* lane_rotation(double pos, const RopeTable& rt, int l, int rope,
-                                                        double2* mine, float* cs, float* sn) {
-    const int first = 4 * l - (8 * LPR - rope) / 2;
+template <class T, int LPR>
+struct RawLane {
+    Row8<T> r[kC];
+    __device__ __forceinline__ void load(const T* p, bool in) {
 #pragma unroll
-    for (int p = 0; p < 4; p++) {
-        cs[p] = 1.f;
-        sn[p] = 0.f;
+        for (int c = 0; c < kC; c++) {
+            r[c].zero();
+            if (in) r[c].load(p + 8 * LPR * c);
+        }
     }
-    if (first < 0) return nullptr;
+    __device__ __forceinline__ void get(Lane& x) const {
 #pragma unroll
-    for (int p = 0; p < 4; p++) {
-        double c, s;
-        rotation(pos, rt.freq[first + p], c, s);
-        mine[p] = make_double2(c, s);
-        cs[p] = (float)c;
-        sn[p] = (float)s;
+        for (int c = 0; c < kC; c++) r[c].get(x.v[c]);
     }
-    return mine;
-}
+};
 
 struct QueryArgs {
     const void* q;
@@ -445,7 +502,7 @@ struct QueryArgs {
 
 template <class T, int LPR, bool FP4>
 __global__ void __launch_bounds__(32 * kWarps) indexer_queries_kernel(const QueryArgs a, const RopeTable rt) {
-    __shared__ double2 rot64[32 * kWarps][4];
+    __shared__ double2 rot64[32 * kWarps][4 * kC];
     pdl_wait();
     const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
     constexpr int kRows = 32 / LPR;
@@ -454,29 +511,19 @@ __global__ void __launch_bounds__(32 * kWarps) indexer_queries_kernel(const Quer
     if (t >= a.Q) return;
     const int h0 = (int)(task - t * a.warps_per_token) * a.heads_per_warp;
     const int h1 = min(h0 + a.heads_per_warp, a.H);
-    float w[8], cs[4], sn[4];
-    load_weight8(a.weight, 8 * l, w);
-    const bool past = weight_past_range(w);
     const T* src = (const T*)a.q + t * a.st + (h0 + sub) * a.sh + 8 * l;
-    constexpr int kU = 2;                // rows a lane loads ahead of the one it works on
-    Row8<T> r[kU];
-#pragma unroll
-    for (int u = 0; u < kU; u++) {
-        r[u].zero();
-        if (h0 + sub + u * kRows < h1) r[u].load(src + u * kRows * a.sh);
-    }
-    const double2* rot = lane_rotation<LPR>((double)a.pos[t], rt, l, a.rope, rot64[threadIdx.x], cs, sn);
+    RawLane<T, LPR> cur, nxt;            // the row worked on and the one after it
+    cur.load(src, h0 + sub < h1);
+    LaneParams p;
+    lane_params<LPR>(p, a.weight, (double)a.pos[t], rt, l, a.rope, rot64[threadIdx.x]);
     int64_t dst = t * a.H + h0 + sub;
-    for (int hb = h0; hb < h1; hb += kRows) {
-        const int h = hb + sub;
-        float x[8];
-        r[0].get(x);
-#pragma unroll
-        for (int u = 0; u + 1 < kU; u++) r[u] = r[u + 1];
-        r[kU - 1].zero();
+    for (int h = h0 + sub; h - sub < h1; h += kRows) {
         src += kRows * a.sh;
-        if (h + kU * kRows < h1) r[kU - 1].load(src + (kU - 1) * kRows * a.sh);
-        quantize_row<LPR, FP4>(x, l, cs, sn, rot, w, past, a.norm, a.eps, a.o, dst, h < h1);
+        nxt.load(src, h + kRows < h1);
+        Lane x;
+        cur.get(x);
+        quantize_row<LPR, FP4>(x, l, p, a.norm, a.eps, a.o, dst, h < h1);
+        cur = nxt;
         dst += kRows;
     }
     __threadfence();
@@ -499,17 +546,16 @@ struct AppendArgs {
 // One listed entry per row: its position is the block end (i + 1) m - 1.
 template <class T, int LPR, bool FP4>
 __global__ void __launch_bounds__(32 * kWarps) indexer_append_kernel(const AppendArgs a, const RopeTable rt) {
-    __shared__ double2 rot64[32 * kWarps][4];
+    __shared__ double2 rot64[32 * kWarps][4 * kC];
     pdl_wait();
     const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
     constexpr int kRows = 32 / LPR;
     const int64_t it = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kRows + sub;
     bool in = it < a.n;
     int64_t dst = 0, pos = 0;
-    Row8<T> r;
-    r.zero();
+    RawLane<T, LPR> r;
+    r.load((const T*)a.k + it * a.ld + 8 * l, in);
     if (in) {
-        r.load((const T*)a.k + it * a.ld + 8 * l);
         const int b = a.item_seq[it];
         const int64_t i = a.item_ent[it];
         bool ok = b >= 0 && b < a.B && i >= 0;
@@ -523,14 +569,13 @@ __global__ void __launch_bounds__(32 * kWarps) indexer_append_kernel(const Appen
             if (l == 0) flag(a.o.st, CSA_DEV_OOB);
             in = false;
             pos = 0;
-            r.zero();
         }
     }
-    float w[8], x[8], cs[4], sn[4];
-    load_weight8(a.weight, 8 * l, w);
-    const double2* rot = lane_rotation<LPR>((double)pos, rt, l, a.rope, rot64[threadIdx.x], cs, sn);
+    LaneParams p;
+    lane_params<LPR>(p, a.weight, (double)pos, rt, l, a.rope, rot64[threadIdx.x]);
+    Lane x;
     r.get(x);
-    quantize_row<LPR, FP4>(x, l, cs, sn, rot, w, weight_past_range(w), a.norm, a.eps, a.o, dst, in);
+    quantize_row<LPR, FP4>(x, l, p, a.norm, a.eps, a.o, dst, in);
     __threadfence();
 }
 
@@ -581,9 +626,11 @@ cudaError_t run_qk(QkArgs a, const RopeTable& rt, cudaStream_t stream) {
 template <class T>
 cudaError_t run_qk_dims(const QkArgs& a, const RopeTable& rt, cudaStream_t stream) {
     const int chunks = a.D / 8;
+    // two chunks a lane where they fit: what a pass does once per lane (sums across lanes,
+    // addresses) then serves 16 channels, and with rope = D / 2 every lane has one rotated chunk
     if (chunks <= 8) return run_qk<T, 8, 1>(a, rt, stream);
-    if (chunks <= 16) return run_qk<T, 16, 1>(a, rt, stream);
-    if (chunks <= 32) return run_qk<T, 32, 1>(a, rt, stream);
+    if (chunks <= 16) return run_qk<T, 8, 2>(a, rt, stream);
+    if (chunks <= 32) return run_qk<T, 16, 2>(a, rt, stream);
     if (chunks <= 64) return run_qk<T, 32, 2>(a, rt, stream);
     if (chunks <= 96) return run_qk<T, 32, 3>(a, rt, stream);
     return run_qk<T, 32, 4>(a, rt, stream);
@@ -625,16 +672,16 @@ cudaError_t launch_qk_norm_rope(const QkRows& q, const QkRows& k, const int32_t*
         const bool fp4 = fmt == CSA_IDX_MXFP4;                                            \
         if (dtype == CSA_DT_BF16) {                                                       \
             using T = __nv_bfloat16;                                                      \
-            if (D == 128) return fp4 ? RUN<T, 16, true>(ARGS, rt, stream) : RUN<T, 16, false>(ARGS, rt, stream); \
-            return fp4 ? RUN<T, 8, true>(ARGS, rt, stream) : RUN<T, 8, false>(ARGS, rt, stream); \
+            if (D == 128) return fp4 ? RUN<T, 8, true>(ARGS, rt, stream) : RUN<T, 8, false>(ARGS, rt, stream); \
+            return fp4 ? RUN<T, 4, true>(ARGS, rt, stream) : RUN<T, 4, false>(ARGS, rt, stream); \
         }                                                                                 \
         if (dtype == CSA_DT_F16) {                                                        \
             using T = __half;                                                             \
-            if (D == 128) return fp4 ? RUN<T, 16, true>(ARGS, rt, stream) : RUN<T, 16, false>(ARGS, rt, stream); \
-            return fp4 ? RUN<T, 8, true>(ARGS, rt, stream) : RUN<T, 8, false>(ARGS, rt, stream); \
+            if (D == 128) return fp4 ? RUN<T, 8, true>(ARGS, rt, stream) : RUN<T, 8, false>(ARGS, rt, stream); \
+            return fp4 ? RUN<T, 4, true>(ARGS, rt, stream) : RUN<T, 4, false>(ARGS, rt, stream); \
         }                                                                                 \
-        if (D == 128) return fp4 ? RUN<float, 16, true>(ARGS, rt, stream) : RUN<float, 16, false>(ARGS, rt, stream); \
-        return fp4 ? RUN<float, 8, true>(ARGS, rt, stream) : RUN<float, 8, false>(ARGS, rt, stream); \
+        if (D == 128) return fp4 ? RUN<float, 8, true>(ARGS, rt, stream) : RUN<float, 8, false>(ARGS, rt, stream); \
+        return fp4 ? RUN<float, 4, true>(ARGS, rt, stream) : RUN<float, 4, false>(ARGS, rt, stream); \
     } while (0)
 
 cudaError_t launch_indexer_queries(const void* q, int dtype, int64_t st, int64_t sh, const int32_t* pos,

@@ -442,3 +442,29 @@ def test_indexer_queries_past_the_fp32_range(what, fmt):
     L.csa_indexer_queries(x, pos, codes, scale, fmt=fmt, weight=w, eps=eps, dev_status=st)
     _sync(st, L.CSA_DEV_NAN if what == "nan weight" else 0)
     _same(codes, scale, _quant_ref(io.norm_rope(f64(x), pos.cpu().numpy(), f64(w), eps=eps), fmt))
+
+
+@pytest.mark.parametrize("fmt", [L.CSA_IDX_FP8, L.CSA_IDX_MXFP4])
+def test_rows_do_not_depend_on_their_neighbours(fmt):
+    # all heads at once, in other orders and one by one: codes and scales bit for bit
+    g = torch.Generator(device=DEV).manual_seed(78)
+    x = torch.randn((50, 64, 128), generator=g, device=DEV).to(torch.bfloat16)
+    pos = torch.randint(0, 1 << 20, (50,), generator=g, device=DEV, dtype=torch.int32)
+    codes, scale = _store(fmt, (50, 64), 128)
+    L.csa_indexer_queries(x, pos, codes, scale, fmt=fmt)
+    perm = torch.randperm(64, generator=g, device=DEV)
+    c2, s2 = _store(fmt, (50, 64), 128)
+    L.csa_indexer_queries(x[:, perm].contiguous(), pos, c2, s2, fmt=fmt)
+    assert torch.equal(c2, codes[:, perm]) and torch.equal(s2, scale[:, perm])
+    for h in range(0, 64, 7):
+        c1, s1 = _store(fmt, (50, 1), 128)
+        L.csa_indexer_queries(x[:, h:h + 1], pos, c1, s1, fmt=fmt)
+        assert torch.equal(c1, codes[:, h:h + 1]) and torch.equal(s1, scale[:, h:h + 1])
+    # the same rows as keys of entries at the same positions
+    i = torch.arange(50, dtype=torch.int32, device=DEV)
+    pos4 = i * 4 + 3
+    L.csa_indexer_queries(x, pos4, codes, scale, fmt=fmt)
+    k, ks = _store(fmt, (50,), 128)
+    L.csa_indexer_append(x[:, 5], torch.tensor([1000], device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV),
+                         torch.zeros_like(i), i, k, ks, B=1, fmt=fmt)
+    assert torch.equal(k, codes[:, 5]) and torch.equal(ks, scale[:, 5])
