@@ -139,21 +139,25 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const QkArgs 
     const int h0 = (int)(task - t * a.warps_per_token) * a.heads_per_warp;
     const int h1 = min(h0 + a.heads_per_warp, a.q.heads + a.k.heads);
     const int lo = a.D - a.rope;              // first rotated channel (even)
-    float cs[C][4], sn[C][4];
+    // each pair's cosine and sine by one lane, handed on through shared memory
+    __shared__ float2 tables[kWarps][kMaxRopePairs];
+    float2* table = tables[threadIdx.x >> 5];
     const double pos = (double)a.pos[t];
+    for (int j = lane; j < a.rope / 2; j += 32) {
+        double cd, sd;
+        rotation(pos, rt.freq[j], cd, sd);
+        table[j] = make_float2((float)cd, (float)sd);
+    }
+    __syncwarp();
+    float cs[C][4], sn[C][4];
 #pragma unroll
     for (int c = 0; c < C; c++) {
 #pragma unroll
         for (int p = 0; p < 4; p++) {
             const int ch = 8 * (l + LPR * c) + 2 * p;
-            cs[c][p] = 1.f;
-            sn[c][p] = 0.f;
-            if (ch >= lo && ch < a.D) {
-                double cd, sd;
-                rotation(pos, rt.freq[(ch - lo) >> 1], cd, sd);
-                cs[c][p] = (float)cd;
-                sn[c][p] = (float)sd;
-            }
+            const float2 r = ch >= lo && ch < a.D ? table[(ch - lo) >> 1] : make_float2(1.f, 0.f);
+            cs[c][p] = r.x;
+            sn[c][p] = r.y;
         }
     }
     constexpr int kU = C == 1 ? 4 : C == 2 ? 2 : 1;
@@ -170,7 +174,7 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const QkArgs 
 // (or a block's power-of-two scale) next to a rounding border is not left to fp32.  The fast
 // path computes in fp32 and brackets every quotient z by its error bound: if the codes of z -
 // margin and z + margin agree, that code is the one.  If they differ anywhere in the warp's
-// rows (about 1 pass in 60 on normal data), or the values leave the range the bound holds in,
+// rows (about 1 pass in 200 on normal data), or the values leave the range the bound holds in,
 // the rows are done again in fp64.
 //
 // v = x * weight, rotated, is left without the norm's factor r, which joins the scale.  The
@@ -178,15 +182,16 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const QkArgs 
 // elsewhere): the product with the weight, cos or sin, the product with it, the sum: 4 u.
 //   MXFP4: z = v * (r * 2^-e).  The sum of squares takes at most 6 roundings in a lane and
 //   log2(LPR) <= 3 across, the mean and eps 1, of which rsqrt halves 5 u and adds its
-//   2 ulp = 4 u; the product u, the bracket u: 15 u of |v1| + |v2| <= 2 max|v| (a rotation
-//   keeps the pair's length).  The bracket is one margin per block, 2 max|z| kFp4Margin.
+//   2 ulp = 4 u; the product u, the bracket u: 15 u.  (|v1| + |v2| <= 2 max|v|, since a
+//   rotation keeps the pair's length: 30 u bound the block's largest.)
 //   e4m3: z = v * (448 / max|v|), from which r drops out: 4 u, twice 4 u of the largest |v|, u
 //   each of the division, the product, the definition's rounding of the scale to fp32 and the
-//   bracket: 16 u.  The bracket is relative to each element, since the codes near zero are dense.
-// With rows' sums of squares below 2^100, weights below 2^40 and results within 2^-60 .. 2^100
-// nothing overflows, and an underflowed product is below 2^-34 of a quotient's unit, far from
-// every border but zero's, whose sign it keeps.  (An exact zero beside other values always
-// takes the fp64 path of MXFP4, where its bracket has both signs.)
+//   bracket: 16 u.
+// One margin for a whole block of MXFP4, cheaper per element, sent 1 pass in 30 to fp64 and
+// took 68 us where this takes 58 (8192 tokens x 64 heads x 128).  With rows' sums of squares
+// below 2^100, weights below 2^40 and results within 2^-60 .. 2^100 nothing overflows, and an
+// underflowed product is below 2^-34 of a quotient's unit, far from every border but zero's,
+// whose sign it keeps.
 constexpr float kU24 = 5.9604645e-08f;
 constexpr float kFp4Margin = 20.f * kU24;
 constexpr float kFp8Margin = 20.f * kU24;
@@ -215,7 +220,7 @@ struct RowCodes {
 // The row in fp64 from the input's bits to the codes.  Out of line, its arguments by value: an
 // array whose address is taken would live in local memory on the fast path too.
 template <int LPR, bool FP4>
-__device__ __noinline__ RowCodes quantize_row_f64(const Lane x, const Lane w, const double2* rot0,
+__device__ __noinline__ RowCodes quantize_row_f64(const Lane x, const float* weight, const double2* rot0,
                                                   const double2* rot1, bool norm, double eps) {
     constexpr int D = 8 * kC * LPR;
     double y[kC][8];
@@ -232,8 +237,10 @@ __device__ __noinline__ RowCodes quantize_row_f64(const Lane x, const Lane w, co
 #pragma unroll
     for (int c = 0; c < kC; c++) {
         const double2* rot = c ? rot1 : rot0;
+        float w[8];
+        load_weight8(weight, 8 * LPR * c, w);
 #pragma unroll
-        for (int j = 0; j < 8; j++) y[c][j] *= r * (double)w.v[c][j];
+        for (int j = 0; j < 8; j++) y[c][j] *= r * (double)w[j];
         if (rot) {
 #pragma unroll
             for (int p = 0; p < 4; p++) {
@@ -305,13 +312,22 @@ __device__ __noinline__ RowCodes quantize_row_f64(const Lane x, const Lane w, co
     return o;
 }
 
-// What a lane keeps for the rows of one position: weights, its pairs' cosines and sines (fp32;
-// fp64 in shared memory, null for a chunk that is not rotated).
+// cos and sin of a position's pairs (at most 64 of a 128-channel row), in shared memory: fp32 for
+// the fast path, fp64 for the other.  Kept out of registers: with them and the weights there
+// a thread took 128 and the SM held 16 warps.
+struct RotTable {
+    double2 f64[64];
+    float2 f32[64];
+};
+
+// What a lane needs of a position: its weights (null: ones), its chunks' pairs in the table
+// (null: not rotated), whether a weight is past what the fast path's bound holds for.
 struct LaneParams {
-    Lane w;
-    float cs[kC][4], sn[kC][4];
-    const double2* rot[kC];
-    bool past;         // a weight the fast path's bound does not hold for
+    const float* weight;
+    const RotTable* table;
+    int pair[kC];      // first pair of the chunk, negative: not rotated
+    bool past;
+    __device__ __forceinline__ const double2* rot(int c) const { return pair[c] < 0 ? nullptr : table->f64 + pair[c]; }
 };
 
 // One row over LPR = D / 16 lanes (all lanes of the warp call it): norm, rotation, codes and
@@ -339,18 +355,25 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
 #pragma unroll
     for (int c = 0; c < kC; c++) {
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) mul2(v.v[c] + j, x.v[c] + j, p.w.v[c] + j);
-        if constexpr (!FP4) {
+        for (int j = 0; j < 8; j++) v.v[c][j] = x.v[c][j];
+        if (p.weight) {
+            float w[8];
+            load_weight8(p.weight, 8 * LPR * c, w);
 #pragma unroll
-            for (int j = 0; j < 8; j++) mag.v[c][j] = fabsf(v.v[c][j]);
+            for (int j = 0; j < 8; j += 2) mul2(v.v[c] + j, v.v[c] + j, w + j);
         }
-        if (p.rot[c]) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) mag.v[c][j] = fabsf(v.v[c][j]);
+        if (p.pair[c] >= 0) {
+            const float4* t = reinterpret_cast<const float4*>(p.table->f32 + p.pair[c]);
+            const float4 t0 = t[0], t1 = t[1];
+            const float cs[4] = {t0.x, t0.z, t1.x, t1.z}, sn[4] = {t0.y, t0.w, t1.y, t1.w};
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const float a = v.v[c][2 * i], b = v.v[c][2 * i + 1];
-                if constexpr (!FP4) mag.v[c][2 * i] = mag.v[c][2 * i + 1] = fabsf(a) + fabsf(b);
-                v.v[c][2 * i] = fmaf(a, p.cs[c][i], -(b * p.sn[c][i]));
-                v.v[c][2 * i + 1] = fmaf(a, p.sn[c][i], b * p.cs[c][i]);
+                mag.v[c][2 * i] = mag.v[c][2 * i + 1] = fabsf(a) + fabsf(b);
+                v.v[c][2 * i] = fmaf(a, cs[i], -(b * sn[i]));
+                v.v[c][2 * i + 1] = fmaf(a, sn[i], b * cs[i]);
             }
         }
         amax[c] = 0.f;
@@ -375,15 +398,17 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
             q.scale[c] = e;
             q.bad[c] = false;
             const float inv = zero ? 1.f : r * __uint_as_float((254u - e) << 23);     // r * 2^(127 - e)
-            const float inv2[2] = {inv, inv};
-            const float m = 2.f * kFp4Margin * (amax[c] * inv), up[2] = {m, m}, down[2] = {-m, -m};
+            const float inv2[2] = {inv, inv}, m = kFp4Margin * inv;
             float lo[8], hi[8];
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
                 float z[2];
                 mul2(z, v.v[c] + j, inv2);
-                add2(lo + j, z, down);
-                add2(hi + j, z, up);
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    lo[j + i] = fmaf(-mag.v[c][j + i], m, z[i]);
+                    hi[j + i] = fmaf(mag.v[c][j + i], m, z[i]);
+                }
             }
             q.c[c][0] = pack_e2m1x8(lo);
             q.c[c][1] = 0;
@@ -397,7 +422,7 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
         near |= !zero && !(top > kTiny && top * r > kTiny && top * r < kHuge);
         const float inv = zero ? 1.f : 448.f / top;
         const float inv2[2] = {inv, inv};
-        const float m = kFp8Margin * inv, up[2] = {m, m}, down[2] = {-m, -m};
+        const float m = kFp8Margin * inv;
 #pragma unroll
         for (int c = 0; c < kC; c++) {
             float lo[8], hi[8];
@@ -405,8 +430,11 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
             for (int j = 0; j < 8; j += 2) {
                 float z[2];
                 mul2(z, v.v[c] + j, inv2);
-                fma2(lo + j, mag.v[c] + j, down, z);
-                fma2(hi + j, mag.v[c] + j, up, z);
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    lo[j + i] = fmaf(-mag.v[c][j + i], m, z[i]);
+                    hi[j + i] = fmaf(mag.v[c][j + i], m, z[i]);
+                }
             }
             const uint2 a = pack_e4m3x8(lo), b = pack_e4m3x8(hi);
             q.c[c][0] = a.x;
@@ -418,7 +446,7 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
     }
     const unsigned unsettled = __ballot_sync(0xffffffffu, near);
     if (unsettled) {
-        const RowCodes d = quantize_row_f64<LPR, FP4>(x, p.w, p.rot[0], p.rot[1], norm, (double)eps);
+        const RowCodes d = quantize_row_f64<LPR, FP4>(x, p.weight, p.rot(0), p.rot(1), norm, (double)eps);
         // by row: the fp32 scale of a settled neighbour may differ from the fp64 one in its
         // last bits, and a row's result must not depend on the rows beside it
         if (unsettled >> ((threadIdx.x & 31) & ~(LPR - 1)) & ((1u << LPR) - 1u)) q = d;
@@ -446,31 +474,32 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
     }
 }
 
-// The lane's weights and its pairs' rotation at `pos`; mine: its fp64 cosines and sines.
+// The table of a position by `n` lanes (this one is number i of them): a pair per lane.  The lanes
+// that read it synchronise their warp first.
+__device__ __forceinline__ void fill_table(RotTable& t, const RopeTable& rt, double pos, int pairs, int i, int n) {
+    for (int j = i; j < pairs; j += n) {
+        double c, s;
+        rotation(pos, rt.freq[j], c, s);
+        t.f64[j] = make_double2(c, s);
+        t.f32[j] = make_float2((float)c, (float)s);
+    }
+}
+
 template <int LPR>
-__device__ __forceinline__ void lane_params(LaneParams& p, const float* weight, double pos, const RopeTable& rt,
-                                            int l, int rope, double2* mine) {
+__device__ __forceinline__ LaneParams lane_params(const float* weight, const RotTable& table, int l, int rope) {
+    LaneParams p;
+    p.weight = weight ? weight + 8 * l : nullptr;
+    p.table = &table;
     p.past = false;
 #pragma unroll
     for (int c = 0; c < kC; c++) {
-        load_weight8(weight, 8 * (l + LPR * c), p.w.v[c]);
+        float w[8];
+        load_weight8(p.weight, 8 * LPR * c, w);
 #pragma unroll
-        for (int j = 0; j < 8; j++) p.past |= !(fabsf(p.w.v[c][j]) < 1.0995116e+12f);   // 2^40, or a NaN
-        const int first = 4 * (l + LPR * c) - (8 * kC * LPR - rope) / 2;
-        p.rot[c] = first < 0 ? nullptr : mine + 4 * c;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            p.cs[c][i] = 1.f;
-            p.sn[c][i] = 0.f;
-            if (first >= 0) {
-                double cd, sd;
-                rotation(pos, rt.freq[first + i], cd, sd);
-                mine[4 * c + i] = make_double2(cd, sd);
-                p.cs[c][i] = (float)cd;
-                p.sn[c][i] = (float)sd;
-            }
-        }
+        for (int j = 0; j < 8; j++) p.past |= !(fabsf(w[j]) < 1.0995116e+12f);   // 2^40, or a NaN
+        p.pair[c] = 4 * (l + LPR * c) - (8 * kC * LPR - rope) / 2;
     }
+    return p;
 }
 
 template <class T, int LPR>
@@ -502,7 +531,7 @@ struct QueryArgs {
 
 template <class T, int LPR, bool FP4>
 __global__ void __launch_bounds__(32 * kWarps) indexer_queries_kernel(const QueryArgs a, const RopeTable rt) {
-    __shared__ double2 rot64[32 * kWarps][4 * kC];
+    __shared__ RotTable tables[kWarps];
     pdl_wait();
     const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
     constexpr int kRows = 32 / LPR;
@@ -514,8 +543,10 @@ __global__ void __launch_bounds__(32 * kWarps) indexer_queries_kernel(const Quer
     const T* src = (const T*)a.q + t * a.st + (h0 + sub) * a.sh + 8 * l;
     RawLane<T, LPR> cur, nxt;            // the row worked on and the one after it
     cur.load(src, h0 + sub < h1);
-    LaneParams p;
-    lane_params<LPR>(p, a.weight, (double)a.pos[t], rt, l, a.rope, rot64[threadIdx.x]);
+    RotTable& table = tables[threadIdx.x >> 5];
+    fill_table(table, rt, (double)a.pos[t], a.rope / 2, lane, 32);
+    const LaneParams p = lane_params<LPR>(a.weight, table, l, a.rope);
+    __syncwarp();
     int64_t dst = t * a.H + h0 + sub;
     for (int h = h0 + sub; h - sub < h1; h += kRows) {
         src += kRows * a.sh;
@@ -546,10 +577,10 @@ struct AppendArgs {
 // One listed entry per row: its position is the block end (i + 1) m - 1.
 template <class T, int LPR, bool FP4>
 __global__ void __launch_bounds__(32 * kWarps) indexer_append_kernel(const AppendArgs a, const RopeTable rt) {
-    __shared__ double2 rot64[32 * kWarps][4 * kC];
+    constexpr int kRows = 32 / LPR;
+    __shared__ RotTable tables[kWarps * kRows];
     pdl_wait();
     const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
-    constexpr int kRows = 32 / LPR;
     const int64_t it = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kRows + sub;
     bool in = it < a.n;
     int64_t dst = 0, pos = 0;
@@ -571,8 +602,10 @@ __global__ void __launch_bounds__(32 * kWarps) indexer_append_kernel(const Appen
             pos = 0;
         }
     }
-    LaneParams p;
-    lane_params<LPR>(p, a.weight, (double)pos, rt, l, a.rope, rot64[threadIdx.x]);
+    RotTable& table = tables[threadIdx.x / LPR];
+    fill_table(table, rt, (double)pos, a.rope / 2, l, LPR);
+    const LaneParams p = lane_params<LPR>(a.weight, table, l, a.rope);
+    __syncwarp();
     Lane x;
     r.get(x);
     quantize_row<LPR, FP4>(x, l, p, a.norm, a.eps, a.o, dst, in);
