@@ -2,19 +2,19 @@
 // ("DeepSeek-V4 深度分析报告" 3.4: MXFP4 weights and activations; batch-invariant GEMMs without
 // split-K, 3.3).
 //
-// B's rows (the weight's output features) lie on the 128 lanes of the accumulator and A's
-// rows (tokens) on its columns, whatever the batch: a decode step of a few tokens then
-// still streams the weight 128 (or RT) rows at a time, and a result's products are summed in the
-// same order, K ascending, by the same instruction at every batch size.
+// Two kernels, one structure: a decode step's few tokens lie on the accumulator's columns and the
+// weight's rows on its 128 lanes, so that the weight streams 128 (or RT) rows at a time; a
+// larger batch has its tokens on the lanes and 64 to 256 weight rows on the columns.  In both a
+// result is summed over K ascending, K = 64 an instruction, so that its bits do not
+// depend on the batch (tested over both kernels and every tile width).
 //
-//   warp 0 lane 0  TMA producer: per stage of K = 256 the RT weight rows and NT token rows
-//                  (128 bytes each, 128-byte swizzle) and their scale tiles (bulk copies:
-//                  the tiled scale layout is the tensor cores' own);
+//   warp 0 lane 0  TMA producer: per stage of K = 256 the rows of both operands (128 bytes
+//                  each, 128-byte swizzle) and their scale tiles (bulk copies: the tiled
+//                  scale layout is the tensor cores' own);
 //   warp 1         TMEM allocation; lane 0 copies the scales into TMEM (one slot of columns
 //                  per stage: a slot is refilled only after the MMAs that read it) and
-//                  issues tcgen05.mma kind::mxf4.block_scale, K = 64 an instruction;
-//   warps 2-5      epilogue: a thread holds one output feature and walks the tokens; the 32
-//                  lanes of a warp write consecutive features.
+//                  issues tcgen05.mma kind::mxf4.block_scale;
+//   other warps    epilogue (see the kernels).
 //
 // Every wait is bounded; a timeout aborts the CTA, drains its copies and MMAs, frees TMEM and
 // reports CSA_DEV_TIMEOUT.
@@ -205,6 +205,245 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// ---- tokens on the lanes -------------------------------------------------------------------
+// Persistent: CTA c takes the 128-token x CT-feature tiles c, c + grid, ... (tokens fastest, so
+// that neighbours share the weight's rows in L2).  Eight epilogue warps, two per lane quarter,
+// take the accumulator into registers at once (CT / 2 columns a thread) and hand it back, so
+// the next tile's MMAs wait for those loads only; the conversion, a 2 KB transposition per warp
+// in shared memory and the stores of 64 contiguous bytes a row run beside them.
+constexpr int kWideThreads = 320;
+constexpr int kStageRowB = 64;           // bytes of a row per transposition
+
+template <int CT>
+constexpr int wide_stages() {
+    const int s = (224 * 1024 - 8 * 32 * kStageRowB) / stage_bytes<CT>();
+    return s > 8 ? 8 : s;
+}
+template <int CT>
+constexpr int wide_accs() { return CT <= 128 ? 2 : 1; }
+template <int CT>
+constexpr uint32_t wide_tmem_cols() {
+    const int c = wide_accs<CT>() * CT + wide_stages<CT>() * sf_cols<CT>();
+    return c <= 128 ? 128u : c <= 256 ? 256u : 512u;
+}
+
+template <class T>
+__device__ __forceinline__ void pack16(const uint32_t* d, uint4& v) {   // 16 bytes of T from fp32 bits
+    if constexpr (sizeof(T) == 4) {
+        v = make_uint4(d[0], d[1], d[2], d[3]);
+    } else {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) f[j] = __uint_as_float(d[j]);
+        Row8<T> r;
+        r.set(f);
+        v = r.r;
+    }
+}
+
+template <class T, int CT>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    mxfp4_gemm_wide_kernel(const __grid_constant__ CUtensorMap tmap_a,
+                           const __grid_constant__ CUtensorMap tmap_b, const GemmArgs g, const int mtiles,
+                           const int tiles) {
+    using namespace sm100;
+    constexpr int S = wide_stages<CT>(), kTT = token_tiles<CT>(), kAcc = wide_accs<CT>();
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    uint8_t* sA = smem;                                  // [S][128 tokens x 128 B]
+    uint8_t* sB = sA + S * kWTile;                       // [S][CT features x 128 B]
+    uint8_t* sSa = sB + S * CT * kRowB;                  // [S][2][512]
+    uint8_t* sSb = sSa + S * 2 * kSfTile;                // [S][kTT][2][512]
+    uint8_t* sOut = sSb + S * kTT * 2 * kSfTile;         // [8][32 x 64 B]
+    uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 8 * 32 * kStageRowB);
+    uint64_t* empty = full + S;
+    uint64_t* accfull = empty + S;
+    uint64_t* accempty = accfull + kAcc;
+    uint64_t* drain = accempty + kAcc;
+    uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_smem + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nk = (g.K + kStageK - 1) / kStageK;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; s++) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < kAcc; i++) {
+            mbar_init(&accfull[i], 1);
+            mbar_init(&accempty[i], 8);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+        prefetch_tmap(&tmap_a);
+        prefetch_tmap(&tmap_b);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_base_smem, wide_tmem_cols<CT>());
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_base_smem;
+    pdl_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0, n_load = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+                const int m0 = (tile % mtiles) * 128, n0 = (tile / mtiles) * CT;
+                const uint8_t* asf = g.a_sf + (int64_t)(m0 >> 7) * g.kt128 * kSfTile;
+                const uint8_t* bsf = g.b_sf + (int64_t)(n0 >> 7) * g.kt128 * kSfTile;
+                const int tt = kTT == 2 && n0 + 128 < g.N ? 2 : 1;       // weight scale tiles that exist
+                for (int i = 0; i < nk; i++) {
+                    if (!mbar_wait(&empty[s], phase ^ 1, abort_flag, g.st)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sfb = (uint32_t)min(2, g.kt128 - 2 * i) * kSfTile;
+                    mbar_arrive_expect_tx(&full[s], 128 * kRowB + CT * kRowB + sfb * (1 + tt));
+                    tma_load_2d(sA + s * kWTile, &tmap_a, &full[s], i * kRowB, m0);
+                    tma_load_2d(sB + s * CT * kRowB, &tmap_b, &full[s], i * kRowB, n0);
+                    bulk_load(sSa + s * 2 * kSfTile, asf + (int64_t)2 * i * kSfTile, sfb, &full[s]);
+                    for (int t = 0; t < tt; t++)
+                        bulk_load(sSb + (s * kTT + t) * 2 * kSfTile,
+                                  bsf + ((int64_t)t * g.kt128 + 2 * i) * kSfTile, sfb, &full[s]);
+                    n_load++;
+                    if (++s == S) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            for (int i = 0; i < S; i++) {
+                const int cnt = n_load / S + (i < n_load % S ? 1 : 0);
+                if (cnt) mbar_drain(&full[i], (cnt - 1) & 1, g.st);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int s = 0, n_tile = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, n_tile++) {
+                const int acc = n_tile % kAcc;
+                // a 64-feature tile may begin in the middle of its scale tile: 32 rows a column
+                const uint32_t sf_shift = CT < 128 ? (uint32_t)((tile / mtiles) * CT & 127) >> 5 : 0u;
+                const uint32_t d = tmem + (uint32_t)(acc * CT);
+                if (!mbar_wait(&accempty[acc], ((n_tile / kAcc) & 1) ^ 1, abort_flag, g.st)) break;
+                tc_fence_after();
+                for (int i = 0; i < nk; i++) {
+                    if (!mbar_wait(&full[s], phase, abort_flag, g.st)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int kleft = g.K - i * kStageK;
+                    const uint32_t sfa = tmem + (uint32_t)(kAcc * CT + s * sf_cols<CT>()), sfb = sfa + 8;
+#pragma unroll
+                    for (int kt = 0; kt < 2; kt++)
+                        if (128 * kt < kleft) {
+                            tmem_cp_32x128b_x4(sfa + 4 * kt, smem_desc_rows16(sSa + (s * 2 + kt) * kSfTile));
+#pragma unroll
+                            for (int t = 0; t < kTT; t++)
+                                tmem_cp_32x128b_x4(sfb + 4 * (kt * kTT + t),
+                                                   smem_desc_rows16(sSb + ((s * kTT + t) * 2 + kt) * kSfTile));
+                        }
+                    const uint64_t ad = smem_desc_k_sw128(sA + s * kWTile);
+                    const uint64_t bd = smem_desc_k_sw128(sB + s * CT * kRowB);
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        if (64 * j < kleft) {
+                            const uint32_t id = 2 * (j & 1), sel = id << 30;
+                            mma_mxf4(d, ad + 2 * j, bd + 2 * j, instr_desc_mxf4(128, CT, id, id),
+                                     (sfa + 4 * (j >> 1)) | sel, (sfb + 4 * kTT * (j >> 1) + sf_shift) | sel,
+                                     i > 0 || j > 0 ? 1u : 0u);
+                        }
+                    mma_commit(&empty[s]);
+                    if (++s == S) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (ok) mma_commit(&accfull[acc]);
+            }
+            mma_commit(drain);
+            mbar_drain(drain, 0, g.st);
+        }
+    } else {
+        constexpr int kCols = CT / 2;                        // columns of this warp
+        constexpr int kPiece = 16 / (int)sizeof(T);          // elements of 16 bytes
+        constexpr int kChunk = kStageRowB / (int)sizeof(T);  // columns per transposition
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        uint8_t* stage = sOut + (warp - 2) * 32 * kStageRowB;
+        T* out = reinterpret_cast<T*>(g.out);
+        const bool vec = (reinterpret_cast<uintptr_t>(g.out) | (uintptr_t)(g.ld * (int64_t)sizeof(T))) % 16 == 0;
+        int n_tile = 0;
+        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, n_tile++) {
+            const int acc = n_tile % kAcc;
+            if (!mbar_wait_warp(&accfull[acc], (n_tile / kAcc) & 1, abort_flag, g.st)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * CT + half * kCols);
+            uint32_t d[kCols];
+#pragma unroll
+            for (int c = 0; c < kCols; c += 32) tmem_ld32(taddr + c, d + c);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&accempty[acc]);
+            const int m0 = (tile % mtiles) * 128 + quarter * 32, n0 = (tile / mtiles) * CT + half * kCols;
+#pragma unroll
+            for (int c = 0; c < kCols; c += kChunk) {
+                // lane = token row: its 4 pieces of 16 bytes, spread over the banks
+#pragma unroll
+                for (int p = 0; p < 4; p++) {
+                    uint4 v;
+                    pack16<T>(d + c + p * kPiece, v);
+                    *reinterpret_cast<uint4*>(stage + lane * kStageRowB + ((p ^ ((lane >> 1) & 3)) << 4)) = v;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int r = i * 8 + (lane >> 2), p = lane & 3;
+                    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * kStageRowB + ((p ^ ((r >> 1) & 3)) << 4));
+                    const int n = n0 + c + p * kPiece;
+                    if (m0 + r < g.M && n < g.N) {
+                        T* o = out + (int64_t)(m0 + r) * g.ld + n;
+                        if (vec && n + kPiece <= g.N) {
+                            *reinterpret_cast<uint4*>(o) = v;
+                        } else {
+                            const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+                            for (int j = 0; j < kPiece; j++)
+                                if (n + j < g.N) o[j] = e[j];
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        __threadfence();   // visible before the next kernel's reads ahead of its own wait
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, wide_tmem_cols<CT>());
+    }
+}
+
+template <int CT>
+size_t wide_smem_bytes() {
+    return 1024 + (size_t)wide_stages<CT>() * stage_bytes<CT>() + 8 * 32 * kStageRowB +
+           (2 * wide_stages<CT>() + 2 * wide_accs<CT>() + 1) * 8 + 16;
+}
+
 template <int NT>
 size_t smem_bytes() {
     return 1024 + (size_t)stages<NT>() * stage_bytes<NT>() + (2 * stages<NT>() + 2) * 8 + 16;
@@ -265,6 +504,31 @@ int sm_count() {
     return n > 0 ? n : 148;
 }
 
+template <class T, int CT>
+cudaError_t run_wide(const uint8_t* a, const uint8_t* b, const GemmArgs& g, int sms, cudaStream_t stream) {
+    CUtensorMap mb, ma;
+    if (!make_map(&mb, b, (uint64_t)g.N, (uint64_t)g.K / 2, (uint32_t)CT) ||
+        !make_map(&ma, a, (uint64_t)g.M, (uint64_t)g.K / 2, 128u))
+        return cudaErrorInvalidValue;
+    const size_t sm = wide_smem_bytes<CT>();
+    cudaError_t e = cudaFuncSetAttribute(mxfp4_gemm_wide_kernel<T, CT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+    if (e != cudaSuccess) return e;
+    const int mtiles = (g.M + 127) / 128;
+    const int64_t tiles = (int64_t)mtiles * ((g.N + CT - 1) / CT);
+    if (tiles > 0x7fffffff - 1024) return cudaErrorInvalidValue;
+    LaunchScope scope(kKMxMatmul, stream);
+    return launch_pdl(mxfp4_gemm_wide_kernel<T, CT>, dim3((unsigned)(tiles < sms ? tiles : sms)),
+                      dim3(kWideThreads), sm, stream, ma, mb, g, mtiles, (int)tiles);
+}
+
+template <int CT>
+cudaError_t run_wide_type(const uint8_t* a, const uint8_t* b, const GemmArgs& g, int sms, cudaStream_t stream) {
+    if (g.dtype == CSA_DT_BF16) return run_wide<__nv_bfloat16, CT>(a, b, g, sms, stream);
+    if (g.dtype == CSA_DT_F16) return run_wide<__half, CT>(a, b, g, sms, stream);
+    return run_wide<float, CT>(a, b, g, sms, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_mxfp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b,
@@ -272,18 +536,19 @@ cudaError_t launch_mxfp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uin
                                 int64_t ld, int32_t* st, cudaStream_t stream) {
     const GemmArgs g{a_sf, b_sf, out, ld, st, M, N, K, dtype, (K + 127) / 128};
     const int sms = sm_count();
-    const int NT = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+    if (M > 64) {
+        // the widest feature tile that still gives every SM a tile
+        const int64_t mt = (M + 127) / 128;
+        if (mt * ((N + 255) / 256) >= sms) return run_wide_type<256>(a, b, g, sms, stream);
+        if (mt * ((N + 127) / 128) >= sms) return run_wide_type<128>(a, b, g, sms, stream);
+        return run_wide_type<64>(a, b, g, sms, stream);
+    }
     // weight rows a CTA takes: 128, or fewer while the tiles leave SMs without one
     int RT = 128;
-    const int mt = (M + NT - 1) / NT;
-    while (RT > 32 && (int64_t)((N + RT / 2 - 1) / (RT / 2)) * mt <= sms) RT /= 2;
-    switch (NT) {
-        case 16: return run<16>(a, b, g, RT, stream);
-        case 32: return run<32>(a, b, g, RT, stream);
-        case 64: return run<64>(a, b, g, RT, stream);
-        case 128: return run<128>(a, b, g, RT, stream);
-        default: return run<256>(a, b, g, RT, stream);
-    }
+    while (RT > 32 && (N + RT / 2 - 1) / (RT / 2) <= sms) RT /= 2;
+    if (M <= 16) return run<16>(a, b, g, RT, stream);
+    if (M <= 32) return run<32>(a, b, g, RT, stream);
+    return run<64>(a, b, g, RT, stream);
 }
 
 }  // namespace csa

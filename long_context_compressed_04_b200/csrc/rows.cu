@@ -74,24 +74,28 @@ __device__ __forceinline__ void norm_rope_heads(const QkRows& x, int64_t t, int 
         load_weight8(ch < D ? x.weight : nullptr, ch, w[c]);
     }
     const float inv_d = 1.f / (float)D;
+    const int64_t step = kRows * x.sh, ostep = kRows * x.osh;
     const T* src = (const T*)x.x + t * x.st + (h0 + sub) * x.sh + 8 * l;
     T* dst = (T*)x.out + t * x.ost + (h0 + sub) * x.osh + 8 * l;
-    for (int hb = h0 + sub; hb - sub < h1; hb += kU * kRows) {
+    for (int hb = h0; hb < h1; hb += kU * kRows) {
         Row8<T> r[kU][C];
+        // lanes past the last head load the last one again: no zeroing, no predicate
+        const bool full = hb + kU * kRows <= h1;
 #pragma unroll
-        for (int u = 0; u < kU; u++)
+        for (int u = 0; u < kU; u++) {
+            const T* from = src + u * step;
+            if (!full) from -= max(hb + sub + u * kRows - (h1 - 1), 0) * x.sh;
 #pragma unroll
-            for (int c = 0; c < C; c++) {
-                r[u][c].zero();
-                if (hb + u * kRows < h1 && 8 * (l + LPR * c) < D)
-                    r[u][c].load(src + u * kRows * x.sh + 8 * LPR * c);
-            }
+            for (int c = 0; c < C; c++)
+                if (8 * (l + LPR * c) < D) r[u][c].load(from + 8 * LPR * c);
+        }
 #pragma unroll
         for (int u = 0; u < kU; u++) {
             float f[C][8];
             float s0 = 0.f, s1 = 0.f;
 #pragma unroll
             for (int c = 0; c < C; c++) {
+                if (8 * (l + LPR * c) >= D) r[u][c].zero();
                 r[u][c].get(f[c]);
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
@@ -101,7 +105,7 @@ __device__ __forceinline__ void norm_rope_heads(const QkRows& x, int64_t t, int 
             }
             float rs = 1.f;
             if (norm) rs = rsqrtf(fmaf(group_sum<LPR>(s0 + s1), inv_d, eps));
-            const bool in = hb + u * kRows < h1;
+            const bool in = full | (hb + sub + u * kRows < h1);
 #pragma unroll
             for (int c = 0; c < C; c++) {
                 const int ch = 8 * (l + LPR * c);
@@ -120,11 +124,11 @@ __device__ __forceinline__ void norm_rope_heads(const QkRows& x, int64_t t, int 
                 }
                 Row8<T> o;
                 o.set(f[c]);
-                if (in && ch < D) o.store(dst + u * kRows * x.osh + 8 * LPR * c);
+                if (in && ch < D) o.store(dst + u * ostep + 8 * LPR * c);
             }
         }
-        src += kU * kRows * x.sh;
-        dst += kU * kRows * x.osh;
+        src += kU * step;
+        dst += kU * ostep;
     }
 }
 
@@ -330,6 +334,28 @@ struct LaneParams {
     __device__ __forceinline__ const double2* rot(int c) const { return pair[c] < 0 ? nullptr : table->f64 + pair[c]; }
 };
 
+// The brackets of a chunk's quotients v * inv: margin * (mag of the pair, or |v|) to each side.
+__device__ __forceinline__ void bracket(const float* v, const float* mag, bool rotated, float inv, float margin,
+                                        float* lo, float* hi) {
+    const float inv2[2] = {inv, inv};
+    float z[8];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) mul2(z + j, v + j, inv2);
+    if (rotated) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            lo[j] = fmaf(-mag[j >> 1], margin, z[j]);
+            hi[j] = fmaf(mag[j >> 1], margin, z[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            lo[j] = fmaf(-fabsf(v[j]), margin, z[j]);
+            hi[j] = fmaf(fabsf(v[j]), margin, z[j]);
+        }
+    }
+}
+
 // One row over LPR = D / 16 lanes (all lanes of the warp call it): norm, rotation, codes and
 // scale to row `dst`.
 template <int LPR, bool FP4>
@@ -350,8 +376,8 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
         near |= !(ms > kTiny);
         r = rsqrtf(ms);
     }
-    Lane v, mag;
-    float amax[kC];
+    Lane v;
+    float mag[kC][4], amax[kC];      // of a rotated pair: |v1| + |v2| before the rotation
 #pragma unroll
     for (int c = 0; c < kC; c++) {
 #pragma unroll
@@ -362,8 +388,6 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
 #pragma unroll
             for (int j = 0; j < 8; j += 2) mul2(v.v[c] + j, v.v[c] + j, w + j);
         }
-#pragma unroll
-        for (int j = 0; j < 8; j++) mag.v[c][j] = fabsf(v.v[c][j]);
         if (p.pair[c] >= 0) {
             const float4* t = reinterpret_cast<const float4*>(p.table->f32 + p.pair[c]);
             const float4 t0 = t[0], t1 = t[1];
@@ -371,7 +395,7 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const float a = v.v[c][2 * i], b = v.v[c][2 * i + 1];
-                mag.v[c][2 * i] = mag.v[c][2 * i + 1] = fabsf(a) + fabsf(b);
+                mag[c][i] = fabsf(a) + fabsf(b);
                 v.v[c][2 * i] = fmaf(a, cs[i], -(b * sn[i]));
                 v.v[c][2 * i + 1] = fmaf(a, sn[i], b * cs[i]);
             }
@@ -390,58 +414,37 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
             const float top = amax[c] * r;
             const uint32_t ex = __float_as_uint(top) >> 23;
             // the largest magnitude may itself lie next to a power of two
-            near |= !zero && (!(amax[c] > kTiny) || !(top > kTiny && top < kHuge) ||
-                              __float_as_uint(fmaf(top, 2.1f * kFp4Margin, top)) >> 23 != ex ||
-                              __float_as_uint(fmaf(top, -2.1f * kFp4Margin, top)) >> 23 != ex);
+            const float above = fmaf(top, 2.1f * kFp4Margin, top), below = fmaf(top, -2.1f * kFp4Margin, top);
+            near |= !zero & (!(fminf(amax[c], top) > kTiny) | !(top < kHuge) |
+                             ((__float_as_uint(above) ^ __float_as_uint(below)) >> 23 != 0u));
             // a non-finite block is `near`: the bounds only keep the shift in range
             const uint32_t e = zero ? 0u : max(min(ex, 250u), 2u) - 2u;
             q.scale[c] = e;
             q.bad[c] = false;
             const float inv = zero ? 1.f : r * __uint_as_float((254u - e) << 23);     // r * 2^(127 - e)
-            const float inv2[2] = {inv, inv}, m = kFp4Margin * inv;
             float lo[8], hi[8];
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                float z[2];
-                mul2(z, v.v[c] + j, inv2);
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    lo[j + i] = fmaf(-mag.v[c][j + i], m, z[i]);
-                    hi[j + i] = fmaf(mag.v[c][j + i], m, z[i]);
-                }
-            }
+            bracket(v.v[c], mag[c], p.pair[c] >= 0, inv, kFp4Margin * inv, lo, hi);
             q.c[c][0] = pack_e2m1x8(lo);
             q.c[c][1] = 0;
-            near |= !zero && pack_e2m1x8(hi) != q.c[c][0];     // zeros keep their sign in lo
+            near |= !zero & (pack_e2m1x8(hi) != q.c[c][0]);     // zeros keep their sign in lo
         }
     } else {
         float top = fmaxf(amax[0], amax[1]);
 #pragma unroll
         for (int m = 1; m < LPR; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
         const bool zero = top == 0.f;
-        near |= !zero && !(top > kTiny && top * r > kTiny && top * r < kHuge);
+        near |= !zero & (!(fminf(top, top * r) > kTiny) | !(top * r < kHuge));
         const float inv = zero ? 1.f : 448.f / top;
-        const float inv2[2] = {inv, inv};
-        const float m = kFp8Margin * inv;
 #pragma unroll
         for (int c = 0; c < kC; c++) {
             float lo[8], hi[8];
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                float z[2];
-                mul2(z, v.v[c] + j, inv2);
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    lo[j + i] = fmaf(-mag.v[c][j + i], m, z[i]);
-                    hi[j + i] = fmaf(mag.v[c][j + i], m, z[i]);
-                }
-            }
+            bracket(v.v[c], mag[c], p.pair[c] >= 0, inv, kFp8Margin * inv, lo, hi);
             const uint2 a = pack_e4m3x8(lo), b = pack_e4m3x8(hi);
             q.c[c][0] = a.x;
             q.c[c][1] = a.y;
             q.scale[c] = __float_as_uint(zero ? 1.f : (top * r) * (1.f / 448.f));
             q.bad[c] = false;
-            near |= !zero && (a.x != b.x || a.y != b.y);
+            near |= !zero & ((a.x != b.x) | (a.y != b.y));
         }
     }
     const unsigned unsettled = __ballot_sync(0xffffffffu, near);
@@ -505,12 +508,13 @@ __device__ __forceinline__ LaneParams lane_params(const float* weight, const Rot
 template <class T, int LPR>
 struct RawLane {
     Row8<T> r[kC];
-    __device__ __forceinline__ void load(const T* p, bool in) {
+    __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-        for (int c = 0; c < kC; c++) {
-            r[c].zero();
-            if (in) r[c].load(p + 8 * LPR * c);
-        }
+        for (int c = 0; c < kC; c++) r[c].load(p + 8 * LPR * c);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int c = 0; c < kC; c++) r[c].zero();
     }
     __device__ __forceinline__ void get(Lane& x) const {
 #pragma unroll
@@ -530,7 +534,7 @@ struct QueryArgs {
 };
 
 template <class T, int LPR, bool FP4>
-__global__ void __launch_bounds__(32 * kWarps) indexer_queries_kernel(const QueryArgs a, const RopeTable rt) {
+__global__ void __launch_bounds__(32 * kWarps, 5) indexer_queries_kernel(const QueryArgs a, const RopeTable rt) {
     __shared__ RotTable tables[kWarps];
     pdl_wait();
     const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
@@ -540,20 +544,25 @@ __global__ void __launch_bounds__(32 * kWarps) indexer_queries_kernel(const Quer
     if (t >= a.Q) return;
     const int h0 = (int)(task - t * a.warps_per_token) * a.heads_per_warp;
     const int h1 = min(h0 + a.heads_per_warp, a.H);
-    const T* src = (const T*)a.q + t * a.st + (h0 + sub) * a.sh + 8 * l;
-    RawLane<T, LPR> cur, nxt;            // the row worked on and the one after it
-    cur.load(src, h0 + sub < h1);
+    // the row worked on and the one after it; lanes past the last head load the last one again
+    const T* src = (const T*)a.q + t * a.st + 8 * l;
+    RawLane<T, LPR> cur, nxt;
+    cur.load(src + min(h0 + sub, h1 - 1) * a.sh);
     RotTable& table = tables[threadIdx.x >> 5];
     fill_table(table, rt, (double)a.pos[t], a.rope / 2, lane, 32);
     const LaneParams p = lane_params<LPR>(a.weight, table, l, a.rope);
     __syncwarp();
     int64_t dst = t * a.H + h0 + sub;
-    for (int h = h0 + sub; h - sub < h1; h += kRows) {
-        src += kRows * a.sh;
-        nxt.load(src, h + kRows < h1);
+    src += min(h0 + sub + kRows, h1 - 1) * a.sh;
+    const int64_t step = kRows * a.sh;
+#pragma unroll 1
+    for (int hb = h0; hb < h1; hb += kRows) {
+        nxt.load(src);
+        if (hb + 3 * kRows <= h1) src += step;
+        else src += max(min(kRows, h1 - 1 - (hb + sub + kRows)), 0) * a.sh;
         Lane x;
         cur.get(x);
-        quantize_row<LPR, FP4>(x, l, p, a.norm, a.eps, a.o, dst, h < h1);
+        quantize_row<LPR, FP4>(x, l, p, a.norm, a.eps, a.o, dst, hb + sub < h1);
         cur = nxt;
         dst += kRows;
     }
@@ -585,8 +594,9 @@ __global__ void __launch_bounds__(32 * kWarps) indexer_append_kernel(const Appen
     bool in = it < a.n;
     int64_t dst = 0, pos = 0;
     RawLane<T, LPR> r;
-    r.load((const T*)a.k + it * a.ld + 8 * l, in);
+    r.zero();
     if (in) {
+        r.load((const T*)a.k + it * a.ld + 8 * l);
         const int b = a.item_seq[it];
         const int64_t i = a.item_ent[it];
         bool ok = b >= 0 && b < a.B && i >= 0;
@@ -659,11 +669,9 @@ cudaError_t run_qk(QkArgs a, const RopeTable& rt, cudaStream_t stream) {
 template <class T>
 cudaError_t run_qk_dims(const QkArgs& a, const RopeTable& rt, cudaStream_t stream) {
     const int chunks = a.D / 8;
-    // two chunks a lane where they fit: what a pass does once per lane (sums across lanes,
-    // addresses) then serves 16 channels, and with rope = D / 2 every lane has one rotated chunk
     if (chunks <= 8) return run_qk<T, 8, 1>(a, rt, stream);
-    if (chunks <= 16) return run_qk<T, 8, 2>(a, rt, stream);
-    if (chunks <= 32) return run_qk<T, 16, 2>(a, rt, stream);
+    if (chunks <= 16) return run_qk<T, 16, 1>(a, rt, stream);
+    if (chunks <= 32) return run_qk<T, 32, 1>(a, rt, stream);
     if (chunks <= 64) return run_qk<T, 32, 2>(a, rt, stream);
     if (chunks <= 96) return run_qk<T, 32, 3>(a, rt, stream);
     return run_qk<T, 32, 4>(a, rt, stream);
