@@ -488,7 +488,7 @@ static csa_status_t mxfp4_sizes(int64_t rows, int64_t cols) {
     REQUIRE(cols >= 32 && cols % 32 == 0, "%lld columns: must be a positive multiple of 32",
             (long long)cols);
     SUPPORT(cols <= (1 << 20), "%lld columns not supported (up to 2^20)", (long long)cols);
-    SUPPORT(rows <= (1ll << 31) - 256 && rows <= (1ll << 40) / cols,
+    SUPPORT(rows <= (1ll << 31) - 256 && rows <= (1ll << 36) / cols,
             "%lld rows of %lld columns not supported", (long long)rows, (long long)cols);
     return CSA_OK;
 }

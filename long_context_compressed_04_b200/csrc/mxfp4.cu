@@ -7,10 +7,13 @@
 // to the even code, past 6 to 6).  The division is a multiplication by a power of two and so
 // exact: the codes are those of the definition bit for bit, whatever the batch.
 //
-// Both kernels are bound by HBM: a thread takes 8 consecutive elements (16 bytes of bf16, one
-// 4-byte word of codes), so a warp's loads and stores are contiguous, and four lanes share a
-// block (its amax takes two shuffles).  kUnits independent groups of 8 per thread keep
-// enough bytes in flight.
+// Both kernels are bound by HBM.  A lane takes 8 consecutive elements (16 bytes of bf16, one
+// 4-byte word of codes) and four lanes a block (its amax takes two shuffles); a warp takes 256
+// elements of one row, or as many rows of fewer as fit.  Warps are persistent and work
+// on kItems such pieces at once, whose loads go out together: one fence per warp instead of one per
+// piece, and no division per element (27 -> 17 us for an 8192 x 2048 fp32 weight there and back).
+#include <type_traits>
+
 #include "launchers.cuh"
 #include "rows.cuh"
 
@@ -19,7 +22,7 @@ namespace csa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 4;
+constexpr int kItems = 4;
 
 // Where the scale bytes lie: rows x blocks row-major, or tiles of 128 rows x 4 blocks of 512
 // bytes (the tensor cores' layout: row r, block j of a tile at 16 (r mod 32) + 4 (r div 32)
@@ -32,60 +35,122 @@ struct ScaleMap {
         if (!tiled) return r * nblk + j;
         return ((r >> 7) * ktiles + (j >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (j & 3);
     }
+    // from row r, block j to row r + dr, block j + dj (dj a multiple of 4; in the tiled layout both
+    // rows lie in one group of 32)
+    __device__ __forceinline__ int64_t step(int dr, uint32_t dj) const {
+        return tiled ? dr * 16 + (int64_t)(dj >> 2) * 512 : dr * nblk + dj;
+    }
 };
 
-// u / d for u * d < 2^64, by a multiplication with ceil(2^64 / d); d = 1 apart.
-struct FastDiv {
-    uint64_t mul;
-    uint32_t d;
-    __device__ __forceinline__ uint64_t div(uint64_t u) const { return d == 1 ? u : __umul64hi(u, mul); }
+// How a [rows, units] matrix of 8-element units is cut for warps.  A piece is 32 units: 2^lanes
+// lanes to a row (32 at most), 32 >> lanes rows.  A task is kItems pieces: along a row where a row
+// has that many, else down the rows; one division per task, and piece i of it lies at fixed
+// strides from piece 0.
+struct Tasks {
+    int64_t rows;            // rows walked (the tiled layout's padding included)
+    uint32_t units;          // units of a row, likewise
+    uint32_t n, per_row;     // tasks, and how many a row (or group of rows) is cut into
+    uint32_t mul;            // ceil(2^32 / per_row), 0 for 1
+    int lanes, along;        // along: pieces of a task follow one another along the row
+    __device__ __forceinline__ int row_step() const { return along ? 0 : 32 >> lanes; }
+    __device__ __forceinline__ uint32_t unit_step() const { return along ? 32u : 0u; }
+    // the row and unit of this lane in piece 0 of task i
+    __device__ __forceinline__ void at(uint32_t i, int lane, int64_t& row, uint32_t& unit) const {
+        uint32_t g = i, k = 0;
+        if (per_row > 1) {
+            g = __umulhi(i, mul);
+            k = i - g * per_row;
+            if ((int32_t)k < 0) {            // the rounded-up reciprocal may be one too far
+                g--;
+                k += per_row;
+            }
+        }
+        unit = ((k * (along ? kItems : 1)) << lanes) + (lane & ((1 << lanes) - 1));
+        row = (int64_t)g * ((32 >> lanes) * (along ? 1 : kItems)) + (lane >> lanes);
+    }
 };
-FastDiv fast_div(uint32_t d) { return {d == 1 ? 0 : ~0ull / d + 1, d}; }
 
-// Units of 8 elements over the grid of rows_u x units_u; the units past rows x cols are those
-// of the tiled layout's padding, which only write a zero scale.
+Tasks make_tasks(int64_t rows_u, int64_t units_u) {
+    Tasks t;
+    t.rows = rows_u;
+    t.units = (uint32_t)units_u;
+    t.lanes = 2;
+    while (t.lanes < 5 && (1 << t.lanes) < units_u) t.lanes++;
+    const int64_t chunks = (units_u + (1 << t.lanes) - 1) >> t.lanes;
+    t.along = chunks >= kItems;
+    t.per_row = (uint32_t)(t.along ? (chunks + kItems - 1) / kItems : chunks);
+    const int64_t rows_per = (32 >> t.lanes) * (t.along ? 1 : kItems);
+    t.n = (uint32_t)((rows_u + rows_per - 1) / rows_per * t.per_row);
+    t.mul = t.per_row > 1 ? (uint32_t)((((uint64_t)1 << 32) + t.per_row - 1) / t.per_row) : 0;
+    return t;
+}
+
+// The magnitude bits of the largest of 8 elements as fp32 (a NaN above an infinity above the rest).
+__device__ __forceinline__ uint32_t top_bits(const Row8<float>& v) {
+    float f[8];
+    v.get(f);
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; j++) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+    return top;
+}
+template <class T>
+__device__ __forceinline__ uint32_t top_bits(const Row8<T>& v) {
+    // 16-bit magnitudes compare as integers, two at a time
+    uint32_t m = __vmaxu2(__vmaxu2(v.r.x & 0x7fff7fffu, v.r.y & 0x7fff7fffu),
+                          __vmaxu2(v.r.z & 0x7fff7fffu, v.r.w & 0x7fff7fffu));
+    m = max(m & 0xffffu, m >> 16);
+    if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value)
+        return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+    return m << 16;
+}
+
 template <class T>
 __global__ void __launch_bounds__(kThreads) mxfp4_quantize_kernel(
-    const T* __restrict__ x, int64_t rows, int64_t cols, int64_t ld, int64_t n_units,
-    FastDiv units_per_row, uint32_t* __restrict__ codes, uint8_t* __restrict__ sf, ScaleMap sm,
-    int32_t* __restrict__ st) {
+    const T* __restrict__ x, int64_t rows, uint32_t units, int64_t ld, const Tasks tk,
+    uint32_t* __restrict__ codes, uint8_t* __restrict__ sf, const ScaleMap sm, int32_t* __restrict__ st) {
     pdl_wait();
-    const int64_t u0 = (int64_t)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
-    Row8<T> v[kUnits];
-    int64_t row[kUnits], unit[kUnits];
+    const int lane = threadIdx.x & 31;
+    const int rstep = tk.row_step();
+    const uint32_t ustep = tk.unit_step();
+    const int64_t xstep = rstep * ld + ustep * 8, cstep = (int64_t)rstep * units + ustep;
+    const int64_t sstep = sm.step(rstep, ustep >> 2);
+    for (uint32_t i0 = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i0 < tk.n;
+         i0 += gridDim.x * (kThreads / 32)) {
+        int64_t row;
+        uint32_t unit;
+        tk.at(i0, lane, row, unit);
+        const T* src = x + row * ld + unit * 8;
+        Row8<T> v[kItems];
+        bool in[kItems];
 #pragma unroll
-    for (int i = 0; i < kUnits; i++) {
-        const int64_t u = u0 + (int64_t)i * kThreads;
-        row[i] = (int64_t)units_per_row.div((uint64_t)u);
-        unit[i] = u - row[i] * units_per_row.d;
-        v[i].zero();
-        if (row[i] < rows && unit[i] * 8 < cols) v[i].load(x + row[i] * ld + unit[i] * 8);
-    }
-#pragma unroll
-    for (int i = 0; i < kUnits; i++) {
-        float f[8];
-        v[i].get(f);
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < 8; j++) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int64_t u = u0 + (int64_t)i * kThreads;
-        if (u >= n_units) continue;
-        const uint32_t ex = top >> 23;
-        const bool bad = ex == 255u;               // an infinity or a NaN in the block
-        const uint32_t e = bad ? 255u : ex > 2u ? ex - 2u : 0u;
-        const float inv = __uint_as_float((254u - (bad ? 127u : e)) << 23);   // 2^(127 - e)
-        const bool in = row[i] < rows && unit[i] * 8 < cols;
-        if (in) {
-            float y[8];
-#pragma unroll
-            for (int j = 0; j < 8; j++) y[j] = f[j] * inv;
-            codes[row[i] * (cols >> 3) + unit[i]] = bad ? 0u : pack_e2m1x8(y);
+        for (int i = 0; i < kItems; i++) {
+            in[i] = row + i * rstep < rows && unit + i * ustep < units;
+            v[i].zero();
+            if (in[i]) v[i].load(src + i * xstep);
         }
-        if ((unit[i] & 3) == 0) {
-            sf[sm.at(row[i], unit[i] >> 2)] = (uint8_t)e;
-            if (bad) flag(st, CSA_DEV_NAN);
+        uint32_t* dst = codes + row * units + unit;
+        uint8_t* sfp = sf + sm.at(row, unit >> 2);
+#pragma unroll
+        for (int i = 0; i < kItems; i++) {
+            uint32_t top = top_bits(v[i]);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const uint32_t ex = top >> 23;
+            const bool bad = ex == 255u;               // an infinity or a NaN in the block
+            const uint32_t e = bad ? 255u : max(ex, 2u) - 2u;
+            const float inv = __uint_as_float((254u - (bad ? 127u : e)) << 23);   // 2^(127 - e)
+            const float inv2[2] = {inv, inv};
+            float f[8];
+            v[i].get(f);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) mul2(f + j, f + j, inv2);
+            const uint32_t c = pack_e2m1x8(f);
+            if (in[i]) dst[i * cstep] = bad ? 0u : c;
+            if ((lane & 3) == 0 && row + i * rstep < tk.rows && unit + i * ustep < tk.units) {
+                sfp[i * sstep] = (uint8_t)e;
+                if (bad) flag(st, CSA_DEV_NAN);
+            }
         }
     }
     __threadfence();   // visible before the next kernel's reads ahead of its own wait
@@ -93,63 +158,81 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_kernel(
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) mxfp4_dequantize_kernel(
-    const uint32_t* __restrict__ codes, const uint8_t* __restrict__ sf, ScaleMap sm, int64_t n_units,
-    FastDiv units_per_row, T* __restrict__ out, int64_t ld) {
+    const uint32_t* __restrict__ codes, const uint8_t* __restrict__ sf, const ScaleMap sm, const Tasks tk,
+    T* __restrict__ out, int64_t ld) {
     pdl_wait();
-    const int64_t u0 = (int64_t)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
-    uint32_t c[kUnits], e[kUnits];
-    int64_t row[kUnits], unit[kUnits];
+    const int lane = threadIdx.x & 31;
+    const int rstep = tk.row_step();
+    const uint32_t ustep = tk.unit_step();
+    const int64_t ostep = rstep * ld + ustep * 8, cstep = (int64_t)rstep * tk.units + ustep;
+    const int64_t sstep = sm.step(rstep, ustep >> 2);
+    for (uint32_t i0 = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i0 < tk.n;
+         i0 += gridDim.x * (kThreads / 32)) {
+        int64_t row;
+        uint32_t unit;
+        tk.at(i0, lane, row, unit);
+        const uint32_t* src = codes + row * tk.units + unit;
+        const uint8_t* sfp = sf + sm.at(row, unit >> 2);
+        uint32_t c[kItems], e[kItems];
+        bool in[kItems];
 #pragma unroll
-    for (int i = 0; i < kUnits; i++) {
-        const int64_t u = u0 + (int64_t)i * kThreads;
-        row[i] = (int64_t)units_per_row.div((uint64_t)u);
-        unit[i] = u - row[i] * units_per_row.d;
-        c[i] = e[i] = 0;
-        if (u < n_units) {
-            c[i] = codes[u];
-            e[i] = sf[sm.at(row[i], unit[i] >> 2)];
+        for (int i = 0; i < kItems; i++) {
+            in[i] = row + i * rstep < tk.rows && unit + i * ustep < tk.units;
+            c[i] = e[i] = 0;
+            if (in[i]) {
+                c[i] = src[i * cstep];
+                e[i] = sfp[i * sstep];
+            }
+        }
+        T* dst = out + row * ld + unit * 8;
+#pragma unroll
+        for (int i = 0; i < kItems; i++) {
+            // 2^(e - 127): the byte is the exponent field, 0 the subnormal 2^-127, 255 a NaN
+            const float s = __uint_as_float(e[i] == 0 ? 0x00400000u : e[i] == 255u ? 0x7fffffffu : e[i] << 23);
+            const float s2[2] = {s, s};
+            float f[8];
+            unpack_e2m1x8(c[i], f);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) mul2(f + j, f + j, s2);
+            Row8<T> v;
+            v.set(f);
+            if (in[i]) v.store(dst + i * ostep);
         }
     }
-#pragma unroll
-    for (int i = 0; i < kUnits; i++) {
-        if (u0 + (int64_t)i * kThreads >= n_units) continue;
-        // 2^(e - 127): the byte is the exponent field, 0 the subnormal 2^-127, 255 a NaN
-        const float s = __uint_as_float(e[i] == 0 ? 0x00400000u : e[i] == 255u ? 0x7fffffffu : e[i] << 23);
-        float f[8];
-        unpack_e2m1x8(c[i], f);
-#pragma unroll
-        for (int j = 0; j < 8; j++) f[j] *= s;
-        Row8<T> v;
-        v.set(f);
-        v.store(out + row[i] * ld + unit[i] * 8);
-    }
     __threadfence();
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess)
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n > 0 ? n : 148;
+}
+
+// As many CTAs as are resident, or fewer where the tasks do not fill them.
+dim3 grid_of(const Tasks& t, int per_sm) {
+    const int64_t need = ((int64_t)t.n + kThreads / 32 - 1) / (kThreads / 32);
+    const int64_t most = (int64_t)sm_count() * per_sm;
+    return dim3((unsigned)(need < most ? need : most));
 }
 
 template <class T>
 cudaError_t quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
                      uint8_t* sf, int tiled, int32_t* st, cudaStream_t stream) {
     const int64_t ktiles = (cols + 127) / 128;
-    const int64_t units = tiled ? ktiles * 16 : cols / 8;
-    const int64_t n = units * (tiled ? (rows + 127) / 128 * 128 : rows);
+    const Tasks p = make_tasks(tiled ? (rows + 127) / 128 * 128 : rows, tiled ? ktiles * 16 : cols / 8);
     LaunchScope scope(kKMxQuant, stream);
-    return launch_pdl(mxfp4_quantize_kernel<T>,
-                      dim3((unsigned)((n + kThreads * kUnits - 1) / (kThreads * kUnits))),
-                      dim3(kThreads), 0, stream, (const T*)x, rows, cols, ld, n,
-                      fast_div((uint32_t)units), (uint32_t*)codes, sf,
-                      ScaleMap{tiled, cols / 32, ktiles}, st);
+    return launch_pdl(mxfp4_quantize_kernel<T>, grid_of(p, 4), dim3(kThreads), 0, stream, (const T*)x, rows,
+                      (uint32_t)(cols / 8), ld, p, (uint32_t*)codes, sf, ScaleMap{tiled, cols / 32, ktiles}, st);
 }
 
 template <class T>
 cudaError_t dequantize(const uint8_t* codes, const uint8_t* sf, int tiled, int64_t rows,
                        int64_t cols, void* out, int64_t ld, cudaStream_t stream) {
-    const int64_t n = rows * (cols / 8);
+    const Tasks p = make_tasks(rows, cols / 8);
     LaunchScope scope(kKMxDequant, stream);
-    return launch_pdl(mxfp4_dequantize_kernel<T>,
-                      dim3((unsigned)((n + kThreads * kUnits - 1) / (kThreads * kUnits))),
-                      dim3(kThreads), 0, stream, (const uint32_t*)codes, sf,
-                      ScaleMap{tiled, cols / 32, (cols + 127) / 128}, n,
-                      fast_div((uint32_t)(cols / 8)), (T*)out, ld);
+    return launch_pdl(mxfp4_dequantize_kernel<T>, grid_of(p, 6), dim3(kThreads), 0, stream,
+                      (const uint32_t*)codes, sf, ScaleMap{tiled, cols / 32, (cols + 127) / 128}, p, (T*)out, ld);
 }
 
 }  // namespace
