@@ -50,6 +50,13 @@ constexpr uint32_t tmem_cols() {
     return c <= 128 ? 128u : c <= 256 ? 256u : 512u;
 }
 
+// One lane of a converged warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 struct GemmArgs {
     const uint8_t* a_sf;
     const uint8_t* b_sf;
@@ -139,28 +146,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            bool ok = true;
-            for (int i = 0; i < nk; i++) {
-                const int s = i % S;
-                if (!mbar_wait(&full[s], (i / S) & 1, abort_flag, g.st)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const int kleft = g.K - i * kStageK;
-                const uint32_t sfw = tmem + (uint32_t)(NT + s * sf_cols<NT>()), sfx = sfw + 8;
+        // the whole warp walks the loop, so that the operands of one elected lane's instructions
+        // are uniform
+        bool ok = true;
+        for (int i = 0; i < nk; i++) {
+            const int s = i % S;
+            if (!mbar_wait_warp(&full[s], (i / S) & 1, abort_flag, g.st)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const int kleft = g.K - i * kStageK;
+            const uint32_t sfw = tmem + (uint32_t)(NT + s * sf_cols<NT>()), sfx = sfw + 8;
+            const uint64_t wd = smem_desc_k_sw128(sW + s * kWTile);
+            const uint64_t xd = smem_desc_k_sw128(sX + s * NT * kRowB);
+            const uint64_t swd = smem_desc_rows16(sSw + s * 2 * kSfTile);
+            const uint64_t sxd = smem_desc_rows16(sSx + s * kTT * 2 * kSfTile);
+            if (elect_one()) {
 #pragma unroll
                 for (int kt = 0; kt < 2; kt++)
                     if (128 * kt < kleft) {
-                        tmem_cp_32x128b_x4(sfw + 4 * kt, smem_desc_rows16(sSw + (s * 2 + kt) * kSfTile));
+                        tmem_cp_32x128b_x4(sfw + 4 * kt, swd + (kt * kSfTile >> 4));
 #pragma unroll
                         for (int t = 0; t < kTT; t++)
-                            tmem_cp_32x128b_x4(sfx + 4 * (kt * kTT + t),
-                                               smem_desc_rows16(sSx + ((s * kTT + t) * 2 + kt) * kSfTile));
+                            tmem_cp_32x128b_x4(sfx + 4 * (kt * kTT + t), sxd + ((t * 2 + kt) * kSfTile >> 4));
                     }
-                const uint64_t wd = smem_desc_k_sw128(sW + s * kWTile);
-                const uint64_t xd = smem_desc_k_sw128(sX + s * NT * kRowB);
 #pragma unroll
                 for (int j = 0; j < 4; j++)
                     if (64 * j < kleft) {
@@ -171,10 +181,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 mma_commit(&empty[s]);
             }
+            __syncwarp();
+        }
+        if (elect_one()) {
             if (ok) mma_commit(accfull);
             mma_commit(drain);
             mbar_drain(drain, 0, g.st);
         }
+        __syncwarp();
     } else {
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;       // accumulator lane
@@ -327,36 +341,37 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int s = 0, n_tile = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, n_tile++) {
-                const int acc = n_tile % kAcc;
-                // a 64-feature tile may begin in the middle of its scale tile: 32 rows a column
-                const uint32_t sf_shift = CT < 128 ? (uint32_t)((tile / mtiles) * CT & 127) >> 5 : 0u;
-                const uint32_t d = tmem + (uint32_t)(acc * CT);
-                if (!mbar_wait(&accempty[acc], ((n_tile / kAcc) & 1) ^ 1, abort_flag, g.st)) break;
+        int s = 0, n_tile = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, n_tile++) {
+            const int acc = n_tile % kAcc;
+            // a 64-feature tile may begin in the middle of its scale tile: 32 rows a column
+            const uint32_t sf_shift = CT < 128 ? (uint32_t)((tile / mtiles) * CT & 127) >> 5 : 0u;
+            const uint32_t d = tmem + (uint32_t)(acc * CT);
+            if (!mbar_wait_warp(&accempty[acc], ((n_tile / kAcc) & 1) ^ 1, abort_flag, g.st)) break;
+            tc_fence_after();
+            for (int i = 0; i < nk; i++) {
+                if (!mbar_wait_warp(&full[s], phase, abort_flag, g.st)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
-                for (int i = 0; i < nk; i++) {
-                    if (!mbar_wait(&full[s], phase, abort_flag, g.st)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const int kleft = g.K - i * kStageK;
-                    const uint32_t sfa = tmem + (uint32_t)(kAcc * CT + s * sf_cols<CT>()), sfb = sfa + 8;
+                const int kleft = g.K - i * kStageK;
+                const uint32_t sfa = tmem + (uint32_t)(kAcc * CT + s * sf_cols<CT>()), sfb = sfa + 8;
+                const uint64_t ad = smem_desc_k_sw128(sA + s * kWTile);
+                const uint64_t bd = smem_desc_k_sw128(sB + s * CT * kRowB);
+                const uint64_t sad = smem_desc_rows16(sSa + s * 2 * kSfTile);
+                const uint64_t sbd = smem_desc_rows16(sSb + s * kTT * 2 * kSfTile);
+                if (elect_one()) {
 #pragma unroll
                     for (int kt = 0; kt < 2; kt++)
                         if (128 * kt < kleft) {
-                            tmem_cp_32x128b_x4(sfa + 4 * kt, smem_desc_rows16(sSa + (s * 2 + kt) * kSfTile));
+                            tmem_cp_32x128b_x4(sfa + 4 * kt, sad + (kt * kSfTile >> 4));
 #pragma unroll
                             for (int t = 0; t < kTT; t++)
-                                tmem_cp_32x128b_x4(sfb + 4 * (kt * kTT + t),
-                                                   smem_desc_rows16(sSb + ((s * kTT + t) * 2 + kt) * kSfTile));
+                                tmem_cp_32x128b_x4(sfb + 4 * (kt * kTT + t), sbd + ((t * 2 + kt) * kSfTile >> 4));
                         }
-                    const uint64_t ad = smem_desc_k_sw128(sA + s * kWTile);
-                    const uint64_t bd = smem_desc_k_sw128(sB + s * CT * kRowB);
 #pragma unroll
                     for (int j = 0; j < 4; j++)
                         if (64 * j < kleft) {
@@ -366,16 +381,21 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                      i > 0 || j > 0 ? 1u : 0u);
                         }
                     mma_commit(&empty[s]);
-                    if (++s == S) {
-                        s = 0;
-                        phase ^= 1;
-                    }
                 }
-                if (ok) mma_commit(&accfull[acc]);
+                __syncwarp();
+                if (++s == S) {
+                    s = 0;
+                    phase ^= 1;
+                }
             }
+            if (ok && elect_one()) mma_commit(&accfull[acc]);
+            __syncwarp();
+        }
+        if (elect_one()) {
             mma_commit(drain);
             mbar_drain(drain, 0, g.st);
         }
+        __syncwarp();
     } else {
         constexpr int kCols = CT / 2;                        // columns of this warp
         constexpr int kPiece = 16 / (int)sizeof(T);          // elements of 16 bytes
