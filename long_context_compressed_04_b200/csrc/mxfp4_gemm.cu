@@ -8,13 +8,15 @@
 // result is summed over K ascending, K = 64 an instruction, so that its bits do not
 // depend on the batch (tested over both kernels and every tile width).
 //
-//   warp 0 lane 0  TMA producer: per stage of K = 256 the rows of both operands (128 bytes
+//   warp 0         TMA producer: per stage of K = 256 the rows of both operands (128 bytes
 //                  each, 128-byte swizzle) and their scale tiles (bulk copies: the tiled
 //                  scale layout is the tensor cores' own);
-//   warp 1         TMEM allocation; lane 0 copies the scales into TMEM (one slot of columns
+//   warp 1         TMEM allocation; it copies the scales into TMEM (one slot of columns
 //                  per stage: a slot is refilled only after the MMAs that read it) and
 //                  issues tcgen05.mma kind::mxf4.block_scale;
 //   other warps    epilogue (see the kernels).
+// Warps 0 and 1 walk their loops converged and one elected lane issues: from a branch of one lane
+// each tcgen05 instruction took some 70 clocks to issue (a stage has up to ten).
 //
 // Every wait is bounded; a timeout aborts the CTA, drains its copies and MMAs, frees TMEM and
 // reports CSA_DEV_TIMEOUT.
@@ -121,30 +123,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
 
     if (warp == 0) {
-        if (lane == 0) {
-            const uint8_t* bsf = g.b_sf + (int64_t)(n0 >> 7) * g.kt128 * kSfTile;
-            int n_load = 0;
-            for (int i = 0; i < nk; i++) {
-                const int s = i % S;
-                if (!mbar_wait(&empty[s], ((i / S) & 1) ^ 1, abort_flag, g.st)) break;
-                const uint32_t sfb = (uint32_t)min(2, g.kt128 - 2 * i) * kSfTile;
-                int tt = 0;       // token scale tiles that exist
-                for (int t = 0; t < kTT; t++) tt += m0 + 128 * t < g.M ? 1 : 0;
-                mbar_arrive_expect_tx(&full[s], RT * kRowB + NT * kRowB + sfb * (1 + tt));
+        const uint8_t* bsf = g.b_sf + (int64_t)(n0 >> 7) * g.kt128 * kSfTile;
+        const uint8_t* asf = g.a_sf + (int64_t)(m0 >> 7) * g.kt128 * kSfTile;
+        int n_load = 0;
+        for (int i = 0; i < nk; i++) {
+            const int s = i % S;
+            if (!mbar_wait_warp(&empty[s], ((i / S) & 1) ^ 1, abort_flag, g.st)) break;
+            const uint32_t sfb = (uint32_t)min(2, g.kt128 - 2 * i) * kSfTile;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&full[s], RT * kRowB + NT * kRowB + 2 * sfb);
                 tma_load_2d(sW + s * kWTile + row0 * kRowB, &tmap_b, &full[s], i * kRowB, n0);
                 tma_load_2d(sX + s * NT * kRowB, &tmap_a, &full[s], i * kRowB, m0);
                 bulk_load(sSw + s * 2 * kSfTile, bsf + (int64_t)2 * i * kSfTile, sfb, &full[s]);
-                for (int t = 0; t < tt; t++)
-                    bulk_load(sSx + (s * kTT + t) * 2 * kSfTile,
-                              g.a_sf + ((int64_t)((m0 >> 7) + t) * g.kt128 + 2 * i) * kSfTile, sfb,
-                              &full[s]);
-                n_load++;
+                bulk_load(sSx + s * 2 * kSfTile, asf + (int64_t)2 * i * kSfTile, sfb, &full[s]);
             }
+            __syncwarp();
+            n_load++;
+        }
+        if (lane == 0)
             for (int s = 0; s < S; s++) {
                 const int cnt = n_load / S + (s < n_load % S ? 1 : 0);
                 if (cnt) mbar_drain(&full[s], (cnt - 1) & 1, g.st);
             }
-        }
+        __syncwarp();
     } else if (warp == 1) {
         // the whole warp walks the loop, so that the operands of one elected lane's instructions
         // are uniform
@@ -306,21 +307,21 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     pdl_wait();
 
     if (warp == 0) {
-        if (lane == 0) {
-            int s = 0, n_load = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-                const int m0 = (tile % mtiles) * 128, n0 = (tile / mtiles) * CT;
-                const uint8_t* asf = g.a_sf + (int64_t)(m0 >> 7) * g.kt128 * kSfTile;
-                const uint8_t* bsf = g.b_sf + (int64_t)(n0 >> 7) * g.kt128 * kSfTile;
-                const int tt = kTT == 2 && n0 + 128 < g.N ? 2 : 1;       // weight scale tiles that exist
-                for (int i = 0; i < nk; i++) {
-                    if (!mbar_wait(&empty[s], phase ^ 1, abort_flag, g.st)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sfb = (uint32_t)min(2, g.kt128 - 2 * i) * kSfTile;
+        int s = 0, n_load = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            const int m0 = (tile % mtiles) * 128, n0 = (tile / mtiles) * CT;
+            const uint8_t* asf = g.a_sf + (int64_t)(m0 >> 7) * g.kt128 * kSfTile;
+            const uint8_t* bsf = g.b_sf + (int64_t)(n0 >> 7) * g.kt128 * kSfTile;
+            const int tt = kTT == 2 && n0 + 128 < g.N ? 2 : 1;       // weight scale tiles that exist
+            for (int i = 0; i < nk; i++) {
+                if (!mbar_wait_warp(&empty[s], phase ^ 1, abort_flag, g.st)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sfb = (uint32_t)min(2, g.kt128 - 2 * i) * kSfTile;
+                if (elect_one()) {
                     mbar_arrive_expect_tx(&full[s], 128 * kRowB + CT * kRowB + sfb * (1 + tt));
                     tma_load_2d(sA + s * kWTile, &tmap_a, &full[s], i * kRowB, m0);
                     tma_load_2d(sB + s * CT * kRowB, &tmap_b, &full[s], i * kRowB, n0);
@@ -328,18 +329,21 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     for (int t = 0; t < tt; t++)
                         bulk_load(sSb + (s * kTT + t) * 2 * kSfTile,
                                   bsf + ((int64_t)t * g.kt128 + 2 * i) * kSfTile, sfb, &full[s]);
-                    n_load++;
-                    if (++s == S) {
-                        s = 0;
-                        phase ^= 1;
-                    }
+                }
+                __syncwarp();
+                n_load++;
+                if (++s == S) {
+                    s = 0;
+                    phase ^= 1;
                 }
             }
+        }
+        if (lane == 0)
             for (int i = 0; i < S; i++) {
                 const int cnt = n_load / S + (i < n_load % S ? 1 : 0);
                 if (cnt) mbar_drain(&full[i], (cnt - 1) & 1, g.st);
             }
-        }
+        __syncwarp();
     } else if (warp == 1) {
         int s = 0, n_tile = 0;
         uint32_t phase = 0;
