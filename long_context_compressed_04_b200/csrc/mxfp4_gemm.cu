@@ -561,10 +561,18 @@ cudaError_t launch_mxfp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uin
     const GemmArgs g{a_sf, b_sf, out, ld, st, M, N, K, dtype, (K + 127) / 128};
     const int sms = sm_count();
     if (M > 64) {
-        // the widest feature tile that still gives every SM a tile
-        const int64_t mt = (M + 127) / 128;
-        if (mt * ((N + 255) / 256) >= sms) return run_wide_type<256>(a, b, g, sms, stream);
-        if (mt * ((N + 127) / 128) >= sms) return run_wide_type<128>(a, b, g, sms, stream);
+        // The feature tile that takes the least time: rounds of tiles over the SMs, each a fixed part
+        // and a part per stage of K (in 10 ns, from 8192 x 8192 at K = 512 and 4096: 256 columns
+        // 1.6 + 0.41 per stage, 128 0.7 + 0.28, 64 0.45 + 0.27; the narrow tiles are bound by the
+        // stage's issue, not its bytes).  512 x 8192 x 2048: 10.3 us at 256, 10.8 at 128, 14.0 at
+        // 64; 197 x 4104 x 1504: 10.9, 6.8 and 5.9.
+        const int64_t mt = (M + 127) / 128, nk = (K + kStageK - 1) / kStageK;
+        auto cost = [&](int ct, int64_t fixed, int64_t per_stage) {
+            return (mt * ((N + ct - 1) / ct) + sms - 1) / sms * (fixed + per_stage * nk);
+        };
+        const int64_t c256 = cost(256, 160, 41), c128 = cost(128, 70, 28), c64 = cost(64, 45, 27);
+        if (c256 <= c128 && c256 <= c64) return run_wide_type<256>(a, b, g, sms, stream);
+        if (c128 <= c64) return run_wide_type<128>(a, b, g, sms, stream);
         return run_wide_type<64>(a, b, g, sms, stream);
     }
     // weight rows a CTA takes: 128, or fewer while the tiles leave SMs without one
