@@ -323,8 +323,15 @@ def dense_hca_attn(q, entries, seq_len, ent_off, kv, kv_off, kv_pos0, q_seq, q_p
 # the host time per call is what bounds them); only a failed test looks for the reason.
 _DTYPES = {torch.bfloat16: CSA_DT_BF16, torch.float16: CSA_DT_F16, torch.float32: CSA_DT_F32}
 _U8, _I32T, _I64T, _F32T = torch.uint8, torch.int32, torch.int64, torch.float32
-# the raw handle without a Stream object (3 us less per call), where torch has it
+# The current stream's handle without a Stream object (3 us less per call) and the current
+# device without the check that CUDA is initialised (a CUDA tensor is at hand), where torch has
+# them.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_mx_quantize, _mx_dequantize, _mx_matmul = (_lib.csa_mxfp4_quantize, _lib.csa_mxfp4_dequantize,
+                                            _lib.csa_mxfp4_matmul)
+_qk_norm_rope, _idx_queries, _idx_append = (_lib.csa_qk_norm_rope, _lib.csa_indexer_queries,
+                                            _lib.csa_indexer_append)
 
 
 def _bad(message: str):
@@ -367,24 +374,20 @@ def _need_2d(t, name):
 
 
 def _is_current(dev):
-    return dev >= 0 and dev == torch.cuda.current_device()
+    return dev >= 0 and dev == _device()
 
 
 def _status_ok(t, dev):
     return t is None or (t.dtype is _I32T and t.numel() >= 1 and t.get_device() == dev)
 
 
-def _rows_ok(t):
-    """2-D rows of a known type, contiguous along the last dimension."""
-    return t.dtype in _DTYPES and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)
-
-
-def _dense_ok(t, dtype, shape, dev):
-    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev
+def _dense_ok(t, dtype, n, dev):
+    """n contiguous elements of this type."""
+    return t.dtype is dtype and t.numel() == n and t.is_contiguous() and t.get_device() == dev
 
 
 def _weight_ok(w, D, dev):
-    return w is None or _dense_ok(w, _F32T, (D,), dev)
+    return w is None or _dense_ok(w, _F32T, D, dev)
 
 
 def _ptr(t):
@@ -403,7 +406,7 @@ def csa_mxfp4_sf_bytes(rows: int, cols: int, sf_layout: int = CSA_SF_ROWS) -> in
 
 def _mxfp4_ok(codes, sf, rows, cols, sf_layout, dev):
     need = (rows + 127) // 128 * ((cols + 127) // 128) * 512 if sf_layout else rows * (cols // 32)
-    return (codes.dtype is _U8 and codes.shape == (rows, cols // 2) and codes.is_contiguous()
+    return (codes.dtype is _U8 and codes.numel() == rows * (cols // 2) and codes.is_contiguous()
             and sf.dtype is _U8 and sf.numel() >= need and sf.is_contiguous()
             and codes.get_device() == dev and sf.get_device() == dev)
 
@@ -415,60 +418,78 @@ def _need_mxfp4(codes, sf, rows, cols, sf_layout, what):
         _bad(f"{what} scales must be a contiguous uint8 tensor of at least {need} bytes")
 
 
+def _need_quantized(x, name, codes, sf, sf_layout, dev_status=None):
+    """The reason why x [rows, cols] and its MXFP4 form are refused."""
+    _need_2d(x, name)
+    _need_rows_dtype(x, name)
+    _need_mxfp4(codes, sf, *x.shape, sf_layout, "the")
+    _need_status(dev_status)
+    _need_one_device(x, codes, sf, dev_status)
+
+
 def csa_mxfp4_quantize(x, codes, sf, *, sf_layout: int = CSA_SF_ROWS, dev_status=None,
                        stream=None):
     """Rows of x (bf16, fp16 or fp32 [rows, cols], any row stride) to packed e2m1 codes and
     UE8M0 scales in blocks of 32 (see include/csa.h)."""
-    dev = x.get_device()
-    if not (_rows_ok(x) and _mxfp4_ok(codes, sf, *x.shape, sf_layout, dev)
-            and _status_ok(dev_status, dev) and _is_current(dev)):
+    dev, dtype = x.get_device(), _DTYPES.get(x.dtype)
+    if x.dim() != 2:
         _need_2d(x, "x")
-        _need_rows_dtype(x, "x")
-        _need_mxfp4(codes, sf, *x.shape, sf_layout, "the")
-        _need_status(dev_status)
-        _need_one_device(x, codes, sf, dev_status)
     rows, cols = x.shape
-    _check(_lib.csa_mxfp4_quantize(x.data_ptr(), _DTYPES[x.dtype], rows, cols,
-                                   x.stride(0) if rows > 1 else cols, codes.data_ptr(),
-                                   sf.data_ptr(), sf_layout, _ptr(dev_status),
-                                   _stream_on(stream, dev)))
+    ld, step = x.stride()
+    if not ((step == 1 or cols <= 1) and dtype is not None
+            and _mxfp4_ok(codes, sf, rows, cols, sf_layout, dev)
+            and (dev_status is None or _status_ok(dev_status, dev)) and _is_current(dev)):
+        _need_quantized(x, "x", codes, sf, sf_layout, dev_status)
+    status = _mx_quantize(x.data_ptr(), dtype, rows, cols, ld if rows > 1 else cols,
+                          codes.data_ptr(), sf.data_ptr(), sf_layout,
+                          None if dev_status is None else dev_status.data_ptr(),
+                          _stream_on(stream, dev))
+    if status:
+        _check(status)
 
 
 def csa_mxfp4_dequantize(codes, sf, out, *, sf_layout: int = CSA_SF_ROWS, stream=None):
     """The values MXFP4 rows stand for, into out (bf16, fp16 or fp32 [rows, cols])."""
-    dev = out.get_device()
-    if not (_rows_ok(out) and _mxfp4_ok(codes, sf, *out.shape, sf_layout, dev)
-            and _is_current(dev)):
+    dev, dtype = out.get_device(), _DTYPES.get(out.dtype)
+    if out.dim() != 2:
         _need_2d(out, "out")
-        _need_rows_dtype(out, "out")
-        _need_mxfp4(codes, sf, *out.shape, sf_layout, "the")
-        _need_one_device(codes, sf, out)
     rows, cols = out.shape
-    _check(_lib.csa_mxfp4_dequantize(codes.data_ptr(), sf.data_ptr(), sf_layout, rows, cols,
-                                     out.data_ptr(), _DTYPES[out.dtype],
-                                     out.stride(0) if rows > 1 else cols,
-                                     _stream_on(stream, dev)))
+    ld, step = out.stride()
+    if not ((step == 1 or cols <= 1) and dtype is not None
+            and _mxfp4_ok(codes, sf, rows, cols, sf_layout, dev) and _is_current(dev)):
+        _need_quantized(out, "out", codes, sf, sf_layout)
+    status = _mx_dequantize(codes.data_ptr(), sf.data_ptr(), sf_layout, rows, cols,
+                            out.data_ptr(), dtype, ld if rows > 1 else cols,
+                            _stream_on(stream, dev))
+    if status:
+        _check(status)
 
 
 def csa_mxfp4_matmul(a, a_sf, b, b_sf, out, *, dev_status=None, stream=None):
     """out[m, n] = sum_k A[m, k] B[n, k] of packed MXFP4 a [M, K / 2] and b [N, K / 2] with
     tiled scales (CSA_SF_TILED), out bf16, fp16 or fp32 [M, N] (any row stride)."""
-    dev = out.get_device()
+    dev, dtype = out.get_device(), _DTYPES.get(out.dtype)
+    if out.dim() != 2:
+        _need_2d(out, "out")
+    M, N = out.shape
+    ld, step = out.stride()
     K = 2 * a.shape[-1]
-    if not (_rows_ok(out) and _mxfp4_ok(a, a_sf, out.shape[0], K, CSA_SF_TILED, dev)
-            and _mxfp4_ok(b, b_sf, out.shape[1], K, CSA_SF_TILED, dev)
-            and _status_ok(dev_status, dev) and _is_current(dev)):
+    if not ((step == 1 or N <= 1) and dtype is not None
+            and _mxfp4_ok(a, a_sf, M, K, CSA_SF_TILED, dev)
+            and _mxfp4_ok(b, b_sf, N, K, CSA_SF_TILED, dev)
+            and (dev_status is None or _status_ok(dev_status, dev)) and _is_current(dev)):
         _need_2d(out, "out")
         _need_rows_dtype(out, "out")
-        _need_mxfp4(a, a_sf, out.shape[0], K, CSA_SF_TILED, "a's")
-        _need_mxfp4(b, b_sf, out.shape[1], K, CSA_SF_TILED, "b's")
+        _need_mxfp4(a, a_sf, M, K, CSA_SF_TILED, "a's")
+        _need_mxfp4(b, b_sf, N, K, CSA_SF_TILED, "b's")
         _need_status(dev_status)
         _need_one_device(a, a_sf, b, b_sf, out, dev_status)
-    M, N = out.shape
-    _check(_lib.csa_mxfp4_matmul(a.data_ptr(), a_sf.data_ptr(), b.data_ptr(), b_sf.data_ptr(), M,
-                                 N, K, out.data_ptr(), _DTYPES[out.dtype],
-                                 out.stride(0) if M > 1 else N, _ptr(dev_status),
-                                 _stream_on(stream, dev)))
+    status = _mx_matmul(a.data_ptr(), a_sf.data_ptr(), b.data_ptr(), b_sf.data_ptr(), M, N, K,
+                        out.data_ptr(), dtype, ld if M > 1 else N,
+                        None if dev_status is None else dev_status.data_ptr(),
+                        _stream_on(stream, dev))
+    if status:
+        _check(status)
 
 
 def _need_heads(t, name, T, D):
@@ -477,22 +498,30 @@ def _need_heads(t, name, T, D):
              f"with strides {t.stride()}")
 
 
-def _heads_ok(x, out, dtype, T, D, dev):
-    """Head rows [T, heads, D] and their output."""
-    return (x is None or (out is not None and x.dim() == 3 and x.shape == out.shape
-                          and x.shape[0] == T and x.shape[2] == D and x.dtype is dtype
-                          and out.dtype is dtype and x.get_device() == dev
-                          and out.get_device() == dev and x.stride(2) == 1
-                          and out.stride(2) == 1))
+_NO_HEADS = (None, 0, 0, 0, None, 0, 0)
 
 
-def _head_strides(t, T):
-    """(pointer, token stride, head stride, heads); a lone token's or head's stride is unused."""
-    if t is None:
-        return None, 0, 0, 0
-    st, sh, _ = t.stride()
-    n = t.shape[1]
-    return t.data_ptr(), (st if T > 1 else 0), (sh if n > 1 else 0), n
+def _head_args(x, out, dtype, T, D, dev):
+    """(pointer, token stride, head stride, heads, output's pointer and strides) of head rows
+    [T, heads, D] and their output, None where they do not fit.  A lone token's or head's
+    stride is never used."""
+    if x is None:
+        return _NO_HEADS
+    if out is None or x.dim() != 3:
+        return None
+    t, n, d = shape = x.shape
+    if (t != T or d != D or out.shape != shape or x.dtype is not dtype or out.dtype is not dtype
+            or x.get_device() != dev or out.get_device() != dev):
+        return None
+    st, sh, se = x.stride()
+    ost, osh, ose = out.stride()
+    if se != 1 or ose != 1:
+        return None
+    if T <= 1:
+        st = ost = 0
+    if n <= 1:
+        sh = osh = 0
+    return x.data_ptr(), st, sh, n, out.data_ptr(), ost, osh
 
 
 def csa_qk_norm_rope(q, k, pos, q_out, k_out, *, q_weight=None, k_weight=None, norm: bool = True,
@@ -505,11 +534,13 @@ def csa_qk_norm_rope(q, k, pos, q_out, k_out, *, q_weight=None, k_weight=None, n
     if lead is None:
         _bad("q and k are both None")
     dev, dtype = lead.get_device(), lead.dtype
-    T, D = lead.shape[0], lead.shape[-1]
-    if not (dtype in _DTYPES and _heads_ok(q, q_out, dtype, T, D, dev)
-            and _heads_ok(k, k_out, dtype, T, D, dev) and _dense_ok(pos, _I32T, (T,), dev)
-            and _weight_ok(q_weight, D, dev) and _weight_ok(k_weight, D, dev)
-            and _is_current(dev)):
+    shape = lead.shape
+    T, D = shape[0], shape[-1]
+    qa = _head_args(q, q_out, dtype, T, D, dev)
+    ka = _head_args(k, k_out, dtype, T, D, dev)
+    if not (qa is not None and ka is not None and dtype in _DTYPES
+            and _dense_ok(pos, _I32T, T, dev) and _weight_ok(q_weight, D, dev)
+            and _weight_ok(k_weight, D, dev) and _is_current(dev)):
         _need_rows_dtype(lead, "q" if q is not None else "k")
         for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
             if x is None:
@@ -526,21 +557,23 @@ def csa_qk_norm_rope(q, k, pos, q_out, k_out, *, q_weight=None, k_weight=None, n
                 _need(w, name, _F32T, (D,))
         _need_one_device(lead, k, pos, None if q is None else q_out, None if k is None else k_out,
                          q_weight, k_weight)
-    qp, q_st, q_sh, H = _head_strides(q, T)
-    kp, k_st, k_sh, Hk = _head_strides(k, T)
-    qo, qo_st, qo_sh, _ = _head_strides(None if q is None else q_out, T)
-    ko, ko_st, ko_sh, _ = _head_strides(None if k is None else k_out, T)
-    _check(_lib.csa_qk_norm_rope(qp, q_st, q_sh, kp, k_st, k_sh, pos.data_ptr(), _ptr(q_weight),
-                                 _ptr(k_weight), qo, qo_st, qo_sh, ko, ko_st, ko_sh,
-                                 _DTYPES[dtype], T, H, Hk, D, rope_dims, 1 if norm else 0,
-                                 rope_theta, eps, _stream_on(stream, dev)))
+        _bad("q, k and their outputs must be contiguous along the channels")
+    qp, q_st, q_sh, H, qo, qo_st, qo_sh = qa
+    kp, k_st, k_sh, Hk, ko, ko_st, ko_sh = ka
+    status = _qk_norm_rope(qp, q_st, q_sh, kp, k_st, k_sh, pos.data_ptr(), _ptr(q_weight),
+                           _ptr(k_weight), qo, qo_st, qo_sh, ko, ko_st, ko_sh, _DTYPES[dtype], T,
+                           H, Hk, D, rope_dims, 1 if norm else 0, rope_theta, eps,
+                           _stream_on(stream, dev))
+    if status:
+        _check(status)
 
 
-def _indexer_rows_ok(codes, scale, lead, D, fmt, dev):
+def _indexer_rows_ok(codes, scale, rows, D, fmt, dev):
+    """The codes and scales of `rows` indexer rows."""
     if fmt == CSA_IDX_FP8:
-        return _dense_ok(codes, _U8, (*lead, D), dev) and _dense_ok(scale, _F32T, lead, dev)
-    return _dense_ok(codes, _U8, (*lead, D // 2), dev) and \
-        _dense_ok(scale, _U8, (*lead, D // 32), dev)
+        return _dense_ok(codes, _U8, rows * D, dev) and _dense_ok(scale, _F32T, rows, dev)
+    return _dense_ok(codes, _U8, rows * (D // 2), dev) and \
+        _dense_ok(scale, _U8, rows * (D // 32), dev)
 
 
 def _need_indexer_rows(codes, scale, lead, D, fmt):
@@ -561,9 +594,10 @@ def csa_indexer_queries(q, q_pos, codes, scale, *, fmt: int = CSA_IDX_FP8, weigh
     if q.dim() != 3:
         _bad(f"q must be [Q, H, D], not {tuple(q.shape)}")
     Q, H, D = q.shape
-    dev = q.get_device()
-    if not (q.dtype in _DTYPES and q.stride(2) == 1 and _dense_ok(q_pos, _I32T, (Q,), dev)
-            and _indexer_rows_ok(codes, scale, (Q, H), D, fmt, dev) and _weight_ok(weight, D, dev)
+    st, sh, step = q.stride()
+    dev, dtype = q.get_device(), _DTYPES.get(q.dtype)
+    if not (dtype is not None and step == 1 and _dense_ok(q_pos, _I32T, Q, dev)
+            and _indexer_rows_ok(codes, scale, Q * H, D, fmt, dev) and _weight_ok(weight, D, dev)
             and _status_ok(dev_status, dev) and _is_current(dev)):
         _need_rows_dtype(q, "q")
         _need_heads(q, "q", Q, D)
@@ -573,11 +607,12 @@ def csa_indexer_queries(q, q_pos, codes, scale, *, fmt: int = CSA_IDX_FP8, weigh
             _need(weight, "weight", _F32T, (D,))
         _need_status(dev_status)
         _need_one_device(q, q_pos, codes, scale, weight, dev_status)
-    qp, st, sh, _ = _head_strides(q, Q)
-    _check(_lib.csa_indexer_queries(qp, _DTYPES[q.dtype], st, sh, q_pos.data_ptr(), _ptr(weight),
-                                    1 if norm else 0, rope_dims, rope_theta, eps, Q, H, D, fmt,
-                                    codes.data_ptr(), scale.data_ptr(), _ptr(dev_status),
-                                    _stream_on(stream, dev)))
+    status = _idx_queries(q.data_ptr(), dtype, st if Q > 1 else 0, sh if H > 1 else 0, q_pos.data_ptr(), _ptr(weight),
+                          1 if norm else 0, rope_dims, rope_theta, eps, Q, H, D, fmt,
+                          codes.data_ptr(), scale.data_ptr(), _ptr(dev_status),
+                          _stream_on(stream, dev))
+    if status:
+        _check(status)
 
 
 def csa_indexer_append(k, seq_len, ent_off, item_seq, item_ent, codes, scale, *, B: int,
@@ -587,21 +622,23 @@ def csa_indexer_append(k, seq_len, ent_off, item_seq, item_ent, codes, scale, *,
     """Indexer keys k [n, D] of the listed entries normed, rotated at their block ends,
     quantised and written to their rows of the key store (codes, scale), through the layout's
     block table or ent_off."""
-    dev = k.get_device()
-    bt = getattr(layout, "_block_table", None)
-    if not (_rows_ok(k) and codes.dim() == 2
-            and _indexer_rows_ok(codes, scale, (codes.shape[0],), k.shape[1], fmt, dev)
-            and _dense_ok(item_seq, _I32T, k.shape[:1], dev)
-            and _dense_ok(item_ent, _I32T, k.shape[:1], dev)
-            and _dense_ok(seq_len, _I64T, (B,), dev)
-            and (ent_off is None or _dense_ok(ent_off, _I64T, (B,), dev))
+    dev, dtype = k.get_device(), _DTYPES.get(k.dtype)
+    bt = None if layout is None else getattr(layout, "_block_table", None)
+    if k.dim() != 2:
+        _need_2d(k, "k")
+    n, D = k.shape
+    ld, step = k.stride()
+    ent_rows = codes.shape[0]
+    if not (dtype is not None and step == 1 and codes.dim() == 2
+            and _indexer_rows_ok(codes, scale, ent_rows, D, fmt, dev)
+            and _dense_ok(item_seq, _I32T, n, dev) and _dense_ok(item_ent, _I32T, n, dev)
+            and _dense_ok(seq_len, _I64T, B, dev)
+            and (ent_off is None or _dense_ok(ent_off, _I64T, B, dev))
             and (bt is None or (bt.dtype is _I32T and bt.dim() == 2 and bt.shape[0] >= B
-                                and bt.stride(1) == 1 and bt.get_device() == dev))
-            and _weight_ok(weight, k.shape[1], dev) and _status_ok(dev_status, dev)
-            and _is_current(dev)):
+                                and bt.stride()[1] == 1 and bt.get_device() == dev))
+            and _weight_ok(weight, D, dev) and _status_ok(dev_status, dev) and _is_current(dev)):
         _need_2d(k, "k")
         _need_rows_dtype(k, "k")
-        n, D = k.shape
         _need(item_seq, "item_seq", _I32T, (n,))
         _need(item_ent, "item_ent", _I32T, (n,))
         _need(seq_len, "seq_len", _I64T, (B,))
@@ -616,10 +653,11 @@ def csa_indexer_append(k, seq_len, ent_off, item_seq, item_ent, codes, scale, *,
         _need_status(dev_status)
         _need_one_device(k, seq_len, ent_off, item_seq, item_ent, codes, scale, weight, bt,
                          dev_status)
-    n, D = k.shape
-    _check(_lib.csa_indexer_append(k.data_ptr(), _DTYPES[k.dtype], k.stride(0) if n > 1 else D,
-                                   seq_len.data_ptr(), _ptr(ent_off), item_seq.data_ptr(),
-                                   item_ent.data_ptr(), n, B, m, _ptr(weight), 1 if norm else 0,
-                                   rope_dims, rope_theta, eps, D, fmt, codes.data_ptr(),
-                                   scale.data_ptr(), codes.shape[0], _lay(layout),
-                                   _ptr(dev_status), _stream_on(stream, dev)))
+    status = _idx_append(k.data_ptr(), dtype, ld if n > 1 else D,
+                         seq_len.data_ptr(), _ptr(ent_off), item_seq.data_ptr(),
+                         item_ent.data_ptr(), n, B, m, _ptr(weight), 1 if norm else 0, rope_dims,
+                         rope_theta, eps, D, fmt, codes.data_ptr(), scale.data_ptr(),
+                         ent_rows, _lay(layout), _ptr(dev_status),
+                         _stream_on(stream, dev))
+    if status:
+        _check(status)

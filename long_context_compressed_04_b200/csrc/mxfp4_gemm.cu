@@ -20,6 +20,8 @@
 //
 // Every wait is bounded; a timeout aborts the CTA, drains its copies and MMAs, frees TMEM and
 // reports CSA_DEV_TIMEOUT.
+#include <atomic>
+
 #include "launchers.cuh"
 #include "rows.cuh"
 #include "sm100.cuh"
@@ -506,6 +508,19 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t row_byte
            CUDA_SUCCESS;
 }
 
+// Raises a kernel's shared-memory limit once per device (`done`: a bit per device).
+template <class Kernel>
+cudaError_t allow_smem(Kernel* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 template <int NT>
 cudaError_t run(const uint8_t* a, const uint8_t* b, const GemmArgs& g, int RT, cudaStream_t stream) {
     CUtensorMap mb, ma;
@@ -513,8 +528,8 @@ cudaError_t run(const uint8_t* a, const uint8_t* b, const GemmArgs& g, int RT, c
         !make_map(&ma, a, (uint64_t)g.M, (uint64_t)g.K / 2, (uint32_t)NT))
         return cudaErrorInvalidValue;
     const size_t sm = smem_bytes<NT>();
-    cudaError_t e = cudaFuncSetAttribute(mxfp4_gemm_kernel<NT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(mxfp4_gemm_kernel<NT>, sm, done);
     if (e != cudaSuccess) return e;
     LaunchScope scope(kKMxMatmul, stream);
     return launch_pdl(mxfp4_gemm_kernel<NT>, dim3((g.N + RT - 1) / RT, (g.M + NT - 1) / NT),
@@ -535,8 +550,8 @@ cudaError_t run_wide(const uint8_t* a, const uint8_t* b, const GemmArgs& g, int 
         !make_map(&ma, a, (uint64_t)g.M, (uint64_t)g.K / 2, 128u))
         return cudaErrorInvalidValue;
     const size_t sm = wide_smem_bytes<CT>();
-    cudaError_t e = cudaFuncSetAttribute(mxfp4_gemm_wide_kernel<T, CT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(mxfp4_gemm_wide_kernel<T, CT>, sm, done);
     if (e != cudaSuccess) return e;
     const int mtiles = (g.M + 127) / 128;
     const int64_t tiles = (int64_t)mtiles * ((g.N + CT - 1) / CT);
