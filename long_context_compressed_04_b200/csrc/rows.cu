@@ -208,6 +208,10 @@ struct RowQuant {
     int32_t* st;
 };
 
+// Which of a lane's two chunks are rotated: the second (rope = D / 2), both (rope = D), or as
+// the lane's pair numbers say.
+enum RotMode { kRotAny = 0, kRotUpper = 1, kRotAll = 2 };
+
 // A row's (or a lane's) values: kC chunks of 8 channels, chunk c of lane l at 8 (l + LPR c).
 constexpr int kC = 2;
 struct Lane {
@@ -241,10 +245,8 @@ __device__ __noinline__ RowCodes quantize_row_f64(const Lane x, const float* wei
 #pragma unroll
     for (int c = 0; c < kC; c++) {
         const double2* rot = c ? rot1 : rot0;
-        float w[8];
-        load_weight8(weight, 8 * LPR * c, w);
 #pragma unroll
-        for (int j = 0; j < 8; j++) y[c][j] *= r * (double)w[j];
+        for (int j = 0; j < 8; j++) y[c][j] *= r * (double)__ldg(weight + 8 * LPR * c + j);
         if (rot) {
 #pragma unroll
             for (int p = 0; p < 4; p++) {
@@ -324,43 +326,54 @@ struct RotTable {
     float2 f32[64];
 };
 
-// What a lane needs of a position: its weights (null: ones), its chunks' pairs in the table
-// (null: not rotated), whether a weight is past what the fast path's bound holds for.
+// Weights of a call without any (read like the others: no branch per row).
+#define CSA_ONES_8 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f
+#define CSA_ONES_32 CSA_ONES_8, CSA_ONES_8, CSA_ONES_8, CSA_ONES_8
+__device__ const float kOnes[128] = {CSA_ONES_32, CSA_ONES_32, CSA_ONES_32, CSA_ONES_32};
+
+// What a lane needs of a position: its weights, its chunks' pairs in the table, whether a weight
+// is past what the fast path's bound holds for.
+template <RotMode RM>
 struct LaneParams {
     const float* weight;
     const RotTable* table;
     int pair[kC];      // first pair of the chunk, negative: not rotated
     bool past;
-    __device__ __forceinline__ const double2* rot(int c) const { return pair[c] < 0 ? nullptr : table->f64 + pair[c]; }
+    __device__ __forceinline__ bool rotated(int c) const {
+        return RM == kRotAll || (RM == kRotUpper ? c == 1 : pair[c] >= 0);
+    }
+    __device__ __forceinline__ const double2* rot(int c) const { return rotated(c) ? table->f64 + pair[c] : nullptr; }
 };
 
-// The brackets of a chunk's quotients v * inv: margin * (mag of the pair, or |v|) to each side.
-__device__ __forceinline__ void bracket(const float* v, const float* mag, bool rotated, float inv, float margin,
+// The brackets of a chunk's quotients v * inv: eps * |v * inv| to each side, or for a rotated
+// chunk eps * (mag of the pair) * inv.
+__device__ __forceinline__ void bracket(const float* v, const float* mag, bool rotated, float inv, float eps,
                                         float* lo, float* hi) {
-    const float inv2[2] = {inv, inv};
-    float z[8];
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) mul2(z + j, v + j, inv2);
     if (rotated) {
+        const float inv2[2] = {inv, inv}, m = eps * inv;
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            lo[j] = fmaf(-mag[j >> 1], margin, z[j]);
-            hi[j] = fmaf(mag[j >> 1], margin, z[j]);
+        for (int i = 0; i < 4; i++) {
+            const float d = mag[i] * m, down[2] = {-d, -d}, up[2] = {d, d};
+            float z[2];
+            mul2(z, v + 2 * i, inv2);
+            add2(lo + 2 * i, z, down);
+            add2(hi + 2 * i, z, up);
         }
     } else {
+        const float a = fmaf(inv, -eps, inv), b = fmaf(inv, eps, inv), a2[2] = {a, a}, b2[2] = {b, b};
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            lo[j] = fmaf(-fabsf(v[j]), margin, z[j]);
-            hi[j] = fmaf(fabsf(v[j]), margin, z[j]);
+        for (int j = 0; j < 8; j += 2) {
+            mul2(lo + j, v + j, a2);
+            mul2(hi + j, v + j, b2);
         }
     }
 }
 
 // One row over LPR = D / 16 lanes (all lanes of the warp call it): norm, rotation, codes and
-// scale to row `dst`.
-template <int LPR, bool FP4>
-__device__ __forceinline__ void quantize_row(const Lane& x, int l, const LaneParams& p, bool norm, float eps,
-                                             const RowQuant& o, int64_t dst, bool in) {
+// scale.  codes, scale: this lane's first word and its row's scales.
+template <int LPR, bool FP4, RotMode RM>
+__device__ __forceinline__ void quantize_row(const Lane& x, int l, const LaneParams<RM>& p, bool norm, float eps,
+                                             void* codes, void* scale, int32_t* st, bool in) {
     constexpr int D = 8 * kC * LPR;
     bool near = p.past;         // not settled in fp32
     float s[kC][2] = {};
@@ -370,25 +383,19 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
         for (int j = 0; j < 8; j += 2) fma2(s[c], x.v[c] + j, x.v[c] + j, s[c]);
     const float ss = group_sum<LPR>((s[0][0] + s[0][1]) + (s[1][0] + s[1][1]));   // NaNs and infinities show here
     near |= !(ss < kHuge);
-    float r = 1.f;
-    if (norm) {
-        const float ms = fmaf(ss, 1.f / D, eps);
-        near |= !(ms > kTiny);
-        r = rsqrtf(ms);
-    }
+    const float ms = fmaf(ss, 1.f / D, eps);
+    near |= norm & !(ms > kTiny);
+    const float r = norm ? rsqrtf(ms) : 1.f;
     Lane v;
     float mag[kC][4], amax[kC];      // of a rotated pair: |v1| + |v2| before the rotation
 #pragma unroll
     for (int c = 0; c < kC; c++) {
+        const float4 w0 = __ldg(reinterpret_cast<const float4*>(p.weight + 8 * LPR * c));
+        const float4 w1 = __ldg(reinterpret_cast<const float4*>(p.weight + 8 * LPR * c + 4));
+        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-        for (int j = 0; j < 8; j++) v.v[c][j] = x.v[c][j];
-        if (p.weight) {
-            float w[8];
-            load_weight8(p.weight, 8 * LPR * c, w);
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) mul2(v.v[c] + j, v.v[c] + j, w + j);
-        }
-        if (p.pair[c] >= 0) {
+        for (int j = 0; j < 8; j += 2) mul2(v.v[c] + j, x.v[c] + j, w + j);
+        if (p.rotated(c)) {
             const float4* t = reinterpret_cast<const float4*>(p.table->f32 + p.pair[c]);
             const float4 t0 = t[0], t1 = t[1];
             const float cs[4] = {t0.x, t0.z, t1.x, t1.z}, sn[4] = {t0.y, t0.w, t1.y, t1.w};
@@ -423,7 +430,7 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
             q.bad[c] = false;
             const float inv = zero ? 1.f : r * __uint_as_float((254u - e) << 23);     // r * 2^(127 - e)
             float lo[8], hi[8];
-            bracket(v.v[c], mag[c], p.pair[c] >= 0, inv, kFp4Margin * inv, lo, hi);
+            bracket(v.v[c], mag[c], p.rotated(c), inv, kFp4Margin, lo, hi);
             q.c[c][0] = pack_e2m1x8(lo);
             q.c[c][1] = 0;
             near |= !zero & (pack_e2m1x8(hi) != q.c[c][0]);     // zeros keep their sign in lo
@@ -438,7 +445,7 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
 #pragma unroll
         for (int c = 0; c < kC; c++) {
             float lo[8], hi[8];
-            bracket(v.v[c], mag[c], p.pair[c] >= 0, inv, kFp8Margin * inv, lo, hi);
+            bracket(v.v[c], mag[c], p.rotated(c), inv, kFp8Margin, lo, hi);
             const uint2 a = pack_e4m3x8(lo), b = pack_e4m3x8(hi);
             q.c[c][0] = a.x;
             q.c[c][1] = a.y;
@@ -452,29 +459,31 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
         const RowCodes d = quantize_row_f64<LPR, FP4>(x, p.weight, p.rot(0), p.rot(1), norm, (double)eps);
         // by row: the fp32 scale of a settled neighbour may differ from the fp64 one in its
         // last bits, and a row's result must not depend on the rows beside it
-        if (unsettled >> ((threadIdx.x & 31) & ~(LPR - 1)) & ((1u << LPR) - 1u)) q = d;
+        if (unsettled >> ((threadIdx.x & 31) & ~(LPR - 1)) & ((1u << LPR) - 1u)) {
+            q = d;
+            if (in && ((FP4 ? l & 3 : l) == 0) && (q.bad[0] | q.bad[1])) flag(st, CSA_DEV_NAN);
+        }
     }
     if (!in) return;
     if constexpr (FP4) {
-        uint32_t* codes = reinterpret_cast<uint32_t*>(o.codes) + dst * (D / 8) + l;
-        uint8_t* sf = o.sf + dst * (D / 32) + (l >> 2);
 #pragma unroll
         for (int c = 0; c < kC; c++) {
-            codes[LPR * c] = q.c[c][0];
-            if ((l & 3) == 0) {
-                sf[LPR / 4 * c] = (uint8_t)q.scale[c];
-                if (q.bad[c]) flag(o.st, CSA_DEV_NAN);
-            }
+            reinterpret_cast<uint32_t*>(codes)[LPR * c] = q.c[c][0];
+            if ((l & 3) == 0) reinterpret_cast<uint8_t*>(scale)[LPR / 4 * c] = (uint8_t)q.scale[c];
         }
     } else {
-        uint2* codes = reinterpret_cast<uint2*>(o.codes) + dst * (D / 8) + l;
 #pragma unroll
-        for (int c = 0; c < kC; c++) codes[LPR * c] = make_uint2(q.c[c][0], q.c[c][1]);
-        if (l == 0) {
-            o.scale[dst] = __uint_as_float(q.scale[0]);
-            if (q.bad[0]) flag(o.st, CSA_DEV_NAN);
-        }
+        for (int c = 0; c < kC; c++) reinterpret_cast<uint2*>(codes)[LPR * c] = make_uint2(q.c[c][0], q.c[c][1]);
+        if (l == 0) *reinterpret_cast<float*>(scale) = __uint_as_float(q.scale[0]);
     }
+}
+
+// Where a lane writes row `dst`: its first word of codes, its (first block's) scale.
+template <int LPR, bool FP4>
+__device__ __forceinline__ void lane_out(const RowQuant& o, int64_t dst, int l, uint8_t*& codes, uint8_t*& scale) {
+    constexpr int D = 8 * kC * LPR;
+    codes = o.codes + dst * (FP4 ? D / 2 : D) + l * (FP4 ? 4 : 8);
+    scale = FP4 ? o.sf + dst * (D / 32) + (l >> 2) : reinterpret_cast<uint8_t*>(o.scale + dst);
 }
 
 // The table of a position by `n` lanes (this one is number i of them): a pair per lane.  The lanes
@@ -488,10 +497,10 @@ __device__ __forceinline__ void fill_table(RotTable& t, const RopeTable& rt, dou
     }
 }
 
-template <int LPR>
-__device__ __forceinline__ LaneParams lane_params(const float* weight, const RotTable& table, int l, int rope) {
-    LaneParams p;
-    p.weight = weight ? weight + 8 * l : nullptr;
+template <int LPR, RotMode RM>
+__device__ __forceinline__ LaneParams<RM> lane_params(const float* weight, const RotTable& table, int l, int rope) {
+    LaneParams<RM> p;
+    p.weight = (weight ? weight : kOnes) + 8 * l;
     p.table = &table;
     p.past = false;
 #pragma unroll
@@ -533,7 +542,7 @@ struct QueryArgs {
     RowQuant o;
 };
 
-template <class T, int LPR, bool FP4>
+template <class T, int LPR, bool FP4, RotMode RM>
 __global__ void __launch_bounds__(32 * kWarps, 5) indexer_queries_kernel(const QueryArgs a, const RopeTable rt) {
     __shared__ RotTable tables[kWarps];
     pdl_wait();
@@ -550,9 +559,10 @@ __global__ void __launch_bounds__(32 * kWarps, 5) indexer_queries_kernel(const Q
     cur.load(src + min(h0 + sub, h1 - 1) * a.sh);
     RotTable& table = tables[threadIdx.x >> 5];
     fill_table(table, rt, (double)a.pos[t], a.rope / 2, lane, 32);
-    const LaneParams p = lane_params<LPR>(a.weight, table, l, a.rope);
+    const LaneParams<RM> p = lane_params<LPR, RM>(a.weight, table, l, a.rope);
     __syncwarp();
-    int64_t dst = t * a.H + h0 + sub;
+    uint8_t *codes, *scale;
+    lane_out<LPR, FP4>(a.o, t * a.H + h0 + sub, l, codes, scale);
     src += min(h0 + sub + kRows, h1 - 1) * a.sh;
     const int64_t step = kRows * a.sh;
 #pragma unroll 1
@@ -562,9 +572,10 @@ __global__ void __launch_bounds__(32 * kWarps, 5) indexer_queries_kernel(const Q
         else src += max(min(kRows, h1 - 1 - (hb + sub + kRows)), 0) * a.sh;
         Lane x;
         cur.get(x);
-        quantize_row<LPR, FP4>(x, l, p, a.norm, a.eps, a.o, dst, hb + sub < h1);
+        quantize_row<LPR, FP4, RM>(x, l, p, a.norm, a.eps, codes, scale, a.o.st, hb + sub < h1);
         cur = nxt;
-        dst += kRows;
+        codes += kRows * 8 * kC * LPR / (FP4 ? 2 : 1);
+        scale += kRows * (FP4 ? kC * LPR / 4 : 4);
     }
     __threadfence();
 }
@@ -584,7 +595,7 @@ struct AppendArgs {
 };
 
 // One listed entry per row: its position is the block end (i + 1) m - 1.
-template <class T, int LPR, bool FP4>
+template <class T, int LPR, bool FP4, RotMode RM>
 __global__ void __launch_bounds__(32 * kWarps) indexer_append_kernel(const AppendArgs a, const RopeTable rt) {
     constexpr int kRows = 32 / LPR;
     __shared__ RotTable tables[kWarps * kRows];
@@ -614,11 +625,13 @@ __global__ void __launch_bounds__(32 * kWarps) indexer_append_kernel(const Appen
     }
     RotTable& table = tables[threadIdx.x / LPR];
     fill_table(table, rt, (double)pos, a.rope / 2, l, LPR);
-    const LaneParams p = lane_params<LPR>(a.weight, table, l, a.rope);
+    const LaneParams<RM> p = lane_params<LPR, RM>(a.weight, table, l, a.rope);
     __syncwarp();
+    uint8_t *codes, *scale;
+    lane_out<LPR, FP4>(a.o, dst, l, codes, scale);
     Lane x;
     r.get(x);
-    quantize_row<LPR, FP4>(x, l, p, a.norm, a.eps, a.o, dst, in);
+    quantize_row<LPR, FP4, RM>(x, l, p, a.norm, a.eps, codes, scale, a.o.st, in);
     __threadfence();
 }
 
@@ -677,21 +690,39 @@ cudaError_t run_qk_dims(const QkArgs& a, const RopeTable& rt, cudaStream_t strea
     return run_qk<T, 32, 4>(a, rt, stream);
 }
 
-template <class T, int LPR, bool FP4>
-cudaError_t run_queries(QueryArgs a, const RopeTable& rt, cudaStream_t stream) {
+template <class T, int LPR, bool FP4, RotMode RM>
+cudaError_t run(QueryArgs a, const RopeTable& rt, cudaStream_t stream) {
     split_heads(a.Q, a.H, 32 / LPR, a.heads_per_warp, a.warps_per_token);
     LaunchScope scope(kKIndexerQueries, stream);
-    return launch_pdl(indexer_queries_kernel<T, LPR, FP4>,
+    return launch_pdl(indexer_queries_kernel<T, LPR, FP4, RM>,
                       dim3(blocks_of((int64_t)a.Q * a.warps_per_token)), dim3(32 * kWarps), 0, stream,
                       a, rt);
 }
 
-template <class T, int LPR, bool FP4>
-cudaError_t run_append(const AppendArgs& a, const RopeTable& rt, cudaStream_t stream) {
+template <class T, int LPR, bool FP4, RotMode RM>
+cudaError_t run(const AppendArgs& a, const RopeTable& rt, cudaStream_t stream) {
     constexpr int kRows = 32 / LPR;
     LaunchScope scope(kKIndexerAppend, stream);
-    return launch_pdl(indexer_append_kernel<T, LPR, FP4>, dim3(blocks_of((a.n + kRows - 1) / kRows)),
+    return launch_pdl(indexer_append_kernel<T, LPR, FP4, RM>, dim3(blocks_of((a.n + kRows - 1) / kRows)),
                       dim3(32 * kWarps), 0, stream, a, rt);
+}
+
+// The rotation of half a 128-channel row or of a whole 64-channel one has kernels of its own.
+template <class T, bool FP4, class Args>
+cudaError_t run_dims(int D, const Args& a, const RopeTable& rt, cudaStream_t stream) {
+    if (D == 128)
+        return a.rope == 64 ? run<T, 8, FP4, kRotUpper>(a, rt, stream) : run<T, 8, FP4, kRotAny>(a, rt, stream);
+    return a.rope == 64 ? run<T, 4, FP4, kRotAll>(a, rt, stream) : run<T, 4, FP4, kRotAny>(a, rt, stream);
+}
+
+template <class Args>
+cudaError_t run_types(int dtype, int fmt, int D, const Args& a, const RopeTable& rt, cudaStream_t stream) {
+    const bool fp4 = fmt == CSA_IDX_MXFP4;
+    if (dtype == CSA_DT_BF16)
+        return fp4 ? run_dims<__nv_bfloat16, true>(D, a, rt, stream) : run_dims<__nv_bfloat16, false>(D, a, rt, stream);
+    if (dtype == CSA_DT_F16)
+        return fp4 ? run_dims<__half, true>(D, a, rt, stream) : run_dims<__half, false>(D, a, rt, stream);
+    return fp4 ? run_dims<float, true>(D, a, rt, stream) : run_dims<float, false>(D, a, rt, stream);
 }
 
 }  // namespace
@@ -708,23 +739,6 @@ cudaError_t launch_qk_norm_rope(const QkRows& q, const QkRows& k, const int32_t*
     }
 }
 
-#define CSA_ROWS_DISPATCH(RUN, ARGS)                                                      \
-    do {                                                                                  \
-        const bool fp4 = fmt == CSA_IDX_MXFP4;                                            \
-        if (dtype == CSA_DT_BF16) {                                                       \
-            using T = __nv_bfloat16;                                                      \
-            if (D == 128) return fp4 ? RUN<T, 8, true>(ARGS, rt, stream) : RUN<T, 8, false>(ARGS, rt, stream); \
-            return fp4 ? RUN<T, 4, true>(ARGS, rt, stream) : RUN<T, 4, false>(ARGS, rt, stream); \
-        }                                                                                 \
-        if (dtype == CSA_DT_F16) {                                                        \
-            using T = __half;                                                             \
-            if (D == 128) return fp4 ? RUN<T, 8, true>(ARGS, rt, stream) : RUN<T, 8, false>(ARGS, rt, stream); \
-            return fp4 ? RUN<T, 4, true>(ARGS, rt, stream) : RUN<T, 4, false>(ARGS, rt, stream); \
-        }                                                                                 \
-        if (D == 128) return fp4 ? RUN<float, 8, true>(ARGS, rt, stream) : RUN<float, 8, false>(ARGS, rt, stream); \
-        return fp4 ? RUN<float, 4, true>(ARGS, rt, stream) : RUN<float, 4, false>(ARGS, rt, stream); \
-    } while (0)
-
 cudaError_t launch_indexer_queries(const void* q, int dtype, int64_t st, int64_t sh, const int32_t* pos,
                                    const float* weight, int norm, int rope, float theta, float eps,
                                    int Q, int H, int D, int fmt, uint8_t* codes, void* scale,
@@ -732,7 +746,7 @@ cudaError_t launch_indexer_queries(const void* q, int dtype, int64_t st, int64_t
     QueryArgs a{q, weight, pos, st, sh, Q, H, rope, norm, 0, 0, eps,
                 RowQuant{codes, (float*)scale, (uint8_t*)scale, dev_status}};
     const RopeTable& rt = rope_table(rope, theta);
-    CSA_ROWS_DISPATCH(run_queries, a);
+    return run_types(dtype, fmt, D, a, rt, stream);
 }
 
 cudaError_t launch_indexer_append(const void* k, int dtype, int64_t ld, const int64_t* seq_len,
@@ -744,7 +758,7 @@ cudaError_t launch_indexer_append(const void* k, int dtype, int64_t ld, const in
     AppendArgs a{k, weight, ld, seq_len, er, item_seq, item_ent, n, ent_rows, B, m, rope, norm,
                  eps, RowQuant{codes, (float*)scale, (uint8_t*)scale, dev_status}};
     const RopeTable& rt = rope_table(rope, theta);
-    CSA_ROWS_DISPATCH(run_append, a);
+    return run_types(dtype, fmt, D, a, rt, stream);
 }
 
 }  // namespace csa
