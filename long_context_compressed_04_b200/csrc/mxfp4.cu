@@ -105,6 +105,54 @@ __device__ __forceinline__ uint32_t top_bits(const Row8<T>& v) {
     return m << 16;
 }
 
+// A task's strides from piece to piece: elements of the rows, words of the codes, scale bytes.
+struct Steps {
+    int64_t row_elems, code_words, scales;
+};
+
+// One task of the quantiser; kFull: all its pieces lie inside the matrix.
+template <class T, bool kFull>
+__device__ __forceinline__ void quantize_task(const T* src, uint32_t* dst, uint8_t* sfp, const Steps& step, int lane,
+                                              int rstep, uint32_t ustep, int rows_left, uint32_t units_left,
+                                              int pad_rows_left, uint32_t pad_units_left, int32_t* st) {
+    Row8<T> v[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; i++) {
+        if (kFull || (i * rstep < rows_left && i * ustep < units_left)) {
+            v[i].load(src);
+        } else {
+            v[i].zero();
+        }
+        src += step.row_elems;
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; i++) {
+        uint32_t top = top_bits(v[i]);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        uint32_t e = max(top >> 23, 2u) - 2u;
+        const bool bad = e == 253u;                  // an infinity or a NaN in the block
+        const float inv = __uint_as_float((254u - e) << 23);   // 2^(127 - e)
+        const float inv2[2] = {inv, inv};
+        float f[8];
+        v[i].get(f);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) mul2(f + j, f + j, inv2);
+        uint32_t c = pack_e2m1x8(f);
+        if (bad) {
+            c = 0u;
+            e = 255u;
+        }
+        if (kFull || (i * rstep < rows_left && i * ustep < units_left)) *dst = c;
+        if ((lane & 3) == 0 && (kFull || (i * rstep < pad_rows_left && i * ustep < pad_units_left))) {
+            *sfp = (uint8_t)e;
+            if (bad) flag(st, CSA_DEV_NAN);
+        }
+        dst += step.code_words;
+        sfp += step.scales;
+    }
+}
+
 template <class T>
 __global__ void __launch_bounds__(kThreads) mxfp4_quantize_kernel(
     const T* __restrict__ x, int64_t rows, uint32_t units, int64_t ld, const Tasks tk,
@@ -113,47 +161,57 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_kernel(
     const int lane = threadIdx.x & 31;
     const int rstep = tk.row_step();
     const uint32_t ustep = tk.unit_step();
-    const int64_t xstep = rstep * ld + ustep * 8, cstep = (int64_t)rstep * units + ustep;
-    const int64_t sstep = sm.step(rstep, ustep >> 2);
+    const Steps step{rstep * ld + ustep * 8, (int64_t)rstep * units + ustep, sm.step(rstep, ustep >> 2)};
     for (uint32_t i0 = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i0 < tk.n;
          i0 += gridDim.x * (kThreads / 32)) {
         int64_t row;
         uint32_t unit;
         tk.at(i0, lane, row, unit);
+        // what is left from here, at most a task's worth; past the end nothing is
+        const int rows_left = (int)max(min(rows - row, (int64_t)64), (int64_t)0);
+        const int pad_rows_left = (int)max(min(tk.rows - row, (int64_t)64), (int64_t)0);
+        const uint32_t units_left = unit < units ? units - unit : 0u, pad_units_left = unit < tk.units ? tk.units - unit : 0u;
         const T* src = x + row * ld + unit * 8;
-        Row8<T> v[kItems];
-        bool in[kItems];
-#pragma unroll
-        for (int i = 0; i < kItems; i++) {
-            in[i] = row + i * rstep < rows && unit + i * ustep < units;
-            v[i].zero();
-            if (in[i]) v[i].load(src + i * xstep);
-        }
         uint32_t* dst = codes + row * units + unit;
         uint8_t* sfp = sf + sm.at(row, unit >> 2);
-#pragma unroll
-        for (int i = 0; i < kItems; i++) {
-            uint32_t top = top_bits(v[i]);
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const uint32_t ex = top >> 23;
-            const bool bad = ex == 255u;               // an infinity or a NaN in the block
-            const uint32_t e = bad ? 255u : max(ex, 2u) - 2u;
-            const float inv = __uint_as_float((254u - (bad ? 127u : e)) << 23);   // 2^(127 - e)
-            const float inv2[2] = {inv, inv};
-            float f[8];
-            v[i].get(f);
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) mul2(f + j, f + j, inv2);
-            const uint32_t c = pack_e2m1x8(f);
-            if (in[i]) dst[i * cstep] = bad ? 0u : c;
-            if ((lane & 3) == 0 && row + i * rstep < tk.rows && unit + i * ustep < tk.units) {
-                sfp[i * sstep] = (uint8_t)e;
-                if (bad) flag(st, CSA_DEV_NAN);
-            }
-        }
+        const bool full = (kItems - 1) * rstep < rows_left && (kItems - 1) * ustep < units_left;
+        if (__all_sync(0xffffffffu, full))
+            quantize_task<T, true>(src, dst, sfp, step, lane, rstep, ustep, 0, 0, 0, 0, st);
+        else
+            quantize_task<T, false>(src, dst, sfp, step, lane, rstep, ustep, rows_left, units_left, pad_rows_left,
+                                    pad_units_left, st);
     }
     __threadfence();   // visible before the next kernel's reads ahead of its own wait
+}
+
+template <class T, bool kFull>
+__device__ __forceinline__ void dequantize_task(const uint32_t* src, const uint8_t* sfp, T* dst, const Steps& step,
+                                                int rstep, uint32_t ustep, int rows_left, uint32_t units_left) {
+    uint32_t c[kItems], e[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; i++) {
+        c[i] = e[i] = 0;
+        if (kFull || (i * rstep < rows_left && i * ustep < units_left)) {
+            c[i] = *src;
+            e[i] = *sfp;
+        }
+        src += step.code_words;
+        sfp += step.scales;
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; i++) {
+        // 2^(e - 127): the byte is the exponent field, 0 the subnormal 2^-127, 255 a NaN
+        const float s = __uint_as_float(e[i] == 0 ? 0x00400000u : e[i] == 255u ? 0x7fffffffu : e[i] << 23);
+        const float s2[2] = {s, s};
+        float f[8];
+        unpack_e2m1x8(c[i], f);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) mul2(f + j, f + j, s2);
+        Row8<T> v;
+        v.set(f);
+        if (kFull || (i * rstep < rows_left && i * ustep < units_left)) v.store(dst);
+        dst += step.row_elems;
+    }
 }
 
 template <class T>
@@ -164,40 +222,22 @@ __global__ void __launch_bounds__(kThreads) mxfp4_dequantize_kernel(
     const int lane = threadIdx.x & 31;
     const int rstep = tk.row_step();
     const uint32_t ustep = tk.unit_step();
-    const int64_t ostep = rstep * ld + ustep * 8, cstep = (int64_t)rstep * tk.units + ustep;
-    const int64_t sstep = sm.step(rstep, ustep >> 2);
+    const Steps step{rstep * ld + ustep * 8, (int64_t)rstep * tk.units + ustep, sm.step(rstep, ustep >> 2)};
     for (uint32_t i0 = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i0 < tk.n;
          i0 += gridDim.x * (kThreads / 32)) {
         int64_t row;
         uint32_t unit;
         tk.at(i0, lane, row, unit);
+        const int rows_left = (int)max(min(tk.rows - row, (int64_t)64), (int64_t)0);
+        const uint32_t units_left = unit < tk.units ? tk.units - unit : 0u;
         const uint32_t* src = codes + row * tk.units + unit;
         const uint8_t* sfp = sf + sm.at(row, unit >> 2);
-        uint32_t c[kItems], e[kItems];
-        bool in[kItems];
-#pragma unroll
-        for (int i = 0; i < kItems; i++) {
-            in[i] = row + i * rstep < tk.rows && unit + i * ustep < tk.units;
-            c[i] = e[i] = 0;
-            if (in[i]) {
-                c[i] = src[i * cstep];
-                e[i] = sfp[i * sstep];
-            }
-        }
         T* dst = out + row * ld + unit * 8;
-#pragma unroll
-        for (int i = 0; i < kItems; i++) {
-            // 2^(e - 127): the byte is the exponent field, 0 the subnormal 2^-127, 255 a NaN
-            const float s = __uint_as_float(e[i] == 0 ? 0x00400000u : e[i] == 255u ? 0x7fffffffu : e[i] << 23);
-            const float s2[2] = {s, s};
-            float f[8];
-            unpack_e2m1x8(c[i], f);
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) mul2(f + j, f + j, s2);
-            Row8<T> v;
-            v.set(f);
-            if (in[i]) v.store(dst + i * ostep);
-        }
+        const bool full = (kItems - 1) * rstep < rows_left && (kItems - 1) * ustep < units_left;
+        if (__all_sync(0xffffffffu, full))
+            dequantize_task<T, true>(src, sfp, dst, step, rstep, ustep, 0, 0);
+        else
+            dequantize_task<T, false>(src, sfp, dst, step, rstep, ustep, rows_left, units_left);
     }
     __threadfence();
 }

@@ -543,7 +543,7 @@ struct QueryArgs {
 };
 
 template <class T, int LPR, bool FP4, RotMode RM>
-__global__ void __launch_bounds__(32 * kWarps, 5) indexer_queries_kernel(const QueryArgs a, const RopeTable rt) {
+__global__ void __launch_bounds__(32 * kWarps, 7) indexer_queries_kernel(const QueryArgs a, const RopeTable rt) {
     __shared__ RotTable tables[kWarps];
     pdl_wait();
     const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
