@@ -61,6 +61,19 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// A tile of shared memory to global memory by the TMA unit (rows and bytes outside the map are
+// dropped), in a bulk group of its own; the waits are for the issuing lane's groups: all read
+// from shared memory, or all written.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int32_t x, int32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
+        "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+        "r"(sm100::smem_addr(src)), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 struct GemmArgs {
     const uint8_t* a_sf;
     const uint8_t* b_sf;
@@ -261,8 +274,9 @@ __device__ __forceinline__ void pack16(const uint32_t* d, uint4& v) {   // 16 by
 template <class T, int CT>
 __global__ void __launch_bounds__(kWideThreads, 1)
     mxfp4_gemm_wide_kernel(const __grid_constant__ CUtensorMap tmap_a,
-                           const __grid_constant__ CUtensorMap tmap_b, const GemmArgs g, const int mtiles,
-                           const int tiles) {
+                           const __grid_constant__ CUtensorMap tmap_b,
+                           const __grid_constant__ CUtensorMap tmap_out, const GemmArgs g, const int mtiles,
+                           const int tiles, const int tma_out) {
     using namespace sm100;
     constexpr int S = wide_stages<CT>(), kTT = token_tiles<CT>(), kAcc = wide_accs<CT>();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -433,6 +447,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     pack16<T>(d + c + p * kPiece, v);
                     *reinterpret_cast<uint4*>(stage + lane * kStageRowB + ((p ^ ((lane >> 1) & 3)) << 4)) = v;
                 }
+                if (tma_out) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (m0 < g.M && n0 + c < g.N) {
+                        if (elect_one()) tma_store_2d(&tmap_out, stage, (n0 + c) * (int)sizeof(T), m0);
+                    }
+                    bulk_store_wait_read();
+                    __syncwarp();
+                    continue;
+                }
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
@@ -454,6 +478,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 __syncwarp();
             }
         }
+        bulk_store_wait_all();
         __threadfence();   // visible before the next kernel's reads ahead of its own wait
     }
     tc_fence_before();
@@ -495,17 +520,18 @@ EncodeFn encode_fn() {
 
 // Row-major [rows x row_bytes] byte matrix, boxes of box_rows x 128 bytes, 128-byte swizzle;
 // bytes past a row or the last row read as zeros.
-bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows) {
+bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows,
+              uint64_t pitch = 0, uint32_t box_bytes = kRowB,
+              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     EncodeFn enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[2] = {row_bytes, rows};
-    const cuuint64_t strides[1] = {row_bytes};
-    const cuuint32_t box[2] = {(cuuint32_t)kRowB, box_rows};
+    const cuuint64_t strides[1] = {pitch ? pitch : row_bytes};
+    const cuuint32_t box[2] = {box_bytes, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Raises a kernel's shared-memory limit once per device (`done`: a bit per device).
@@ -545,9 +571,17 @@ int sm_count() {
 
 template <class T, int CT>
 cudaError_t run_wide(const uint8_t* a, const uint8_t* b, const GemmArgs& g, int sms, cudaStream_t stream) {
-    CUtensorMap mb, ma;
+    CUtensorMap mb, ma, mo = {};
     if (!make_map(&mb, b, (uint64_t)g.N, (uint64_t)g.K / 2, (uint32_t)CT) ||
         !make_map(&ma, a, (uint64_t)g.M, (uint64_t)g.K / 2, 128u))
+        return cudaErrorInvalidValue;
+    // The TMA unit stores where it can: rows 16-byte aligned and whole 16-byte pieces (it writes a
+    // row's last piece whole, past the row's end), byte columns within an int32.
+    const uint64_t pitch = (uint64_t)g.ld * sizeof(T);
+    const int tma_out = (reinterpret_cast<uintptr_t>(g.out) | pitch | (uint64_t)g.N * sizeof(T)) % 16 == 0 &&
+                        (uint64_t)g.N * sizeof(T) < (1ull << 31) && pitch < (1ull << 40);
+    if (tma_out && !make_map(&mo, g.out, (uint64_t)g.M, (uint64_t)g.N * sizeof(T), 32u, pitch, kStageRowB,
+                             CU_TENSOR_MAP_SWIZZLE_64B))
         return cudaErrorInvalidValue;
     const size_t sm = wide_smem_bytes<CT>();
     static std::atomic<uint64_t> done{0};
@@ -558,7 +592,7 @@ cudaError_t run_wide(const uint8_t* a, const uint8_t* b, const GemmArgs& g, int 
     if (tiles > 0x7fffffff - 1024) return cudaErrorInvalidValue;
     LaunchScope scope(kKMxMatmul, stream);
     return launch_pdl(mxfp4_gemm_wide_kernel<T, CT>, dim3((unsigned)(tiles < sms ? tiles : sms)),
-                      dim3(kWideThreads), sm, stream, ma, mb, g, mtiles, (int)tiles);
+                      dim3(kWideThreads), sm, stream, ma, mb, mo, g, mtiles, (int)tiles, tma_out);
 }
 
 template <int CT>

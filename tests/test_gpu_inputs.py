@@ -145,6 +145,23 @@ def test_matmul_exact_sums_bit_exact(M, N, K, dt):
     assert bool((out[:, N:] == 3.0).all())
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M,N,K,pad", [(70, 64, 256, 0), (129, 200, 96, 8), (300, 264, 2048, 16), (1, 8, 32, 8),
+                                       (257, 4104, 64, 0), (1000, 1112, 320, 24), (2000, 2560, 160, 0)])
+def test_matmul_aligned_rows_bit_exact(M, N, K, pad, dt):
+    # rows of whole 16-byte pieces (the tiles are then stored by the TMA unit): nothing outside
+    # the N columns is written, rows past M neither
+    rng = np.random.default_rng(M + N + K + pad)
+    a, b = _operands(rng, M, N, K, 126, 127)
+    out = torch.full((M + 3, N + pad), 3.0, dtype=DT[dt], device=DEV)
+    st = _status()
+    L.csa_mxfp4_matmul(_gpu(a[0]), _gpu(io.tile_scales(a[1])), _gpu(b[0]), _gpu(io.tile_scales(b[1])),
+                       out[:M, :N], dev_status=st)
+    _sync(st)
+    assert torch.equal(out[:M, :N].cpu(), torch.from_numpy(a[2] @ b[2].T).to(DT[dt]))
+    assert bool((out[:M, N:] == 3.0).all()) and bool((out[M:] == 3.0).all())
+
+
 @pytest.mark.parametrize("M,N,K", [(5, 300, 4096), (200, 256, 1504), (40, 130, 32)])
 def test_matmul_wide_scales(M, N, K):
     # block exponents spread over 2^-12 .. 2^12: sums round.  Accumulating K / 64 instructions'
@@ -468,3 +485,24 @@ def test_rows_do_not_depend_on_their_neighbours(fmt):
     L.csa_indexer_append(x[:, 5], torch.tensor([1000], device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV),
                          torch.zeros_like(i), i, k, ks, B=1, fmt=fmt)
     assert torch.equal(k, codes[:, 5]) and torch.equal(ks, scale[:, 5])
+
+
+@pytest.mark.parametrize("M,N,K", [(8, 4096, 4096), (300, 4096, 4096), (2000, 4096, 2048)])
+def test_matmul_wait_timeout_is_reported_and_recovers(M, N, K):
+    # the kernels' bounded waits with a limit far below a tile load's time (no kernel here runs
+    # in a cluster): the call reports CSA_DEV_TIMEOUT and returns, the next one is exact again
+    rng = np.random.default_rng(9)
+    a, b = _operands(rng, M, N, K, 126, 126)
+    st = _status()
+    torch.cuda.synchronize()
+    L.csa_debug_set_wait_limit(300)
+    try:
+        _matmul(a, b, "f32", st=st)
+        torch.cuda.synchronize()
+    finally:
+        L.csa_debug_set_wait_limit(0)
+    assert int(st.item()) == L.CSA_DEV_TIMEOUT
+    st.zero_()
+    out = _matmul(a, b, "f32", st=st)
+    _sync(st)
+    assert np.array_equal(f64(out), a[2] @ b[2].T)
