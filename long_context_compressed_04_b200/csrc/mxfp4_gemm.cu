@@ -36,18 +36,19 @@ constexpr int kRowB = kStageK / 2;
 constexpr int kWTile = 128 * kRowB;      // a stage's weight rows (the MMA reads 128)
 constexpr int kSfTile = 512;             // scales of 128 rows x 4 blocks
 
+// A stage: 128 rows for the accumulator's lanes and NT for its columns, with their scale tiles.
 template <int NT>
-constexpr int token_tiles() { return NT > 128 ? 2 : 1; }   // 128-row scale tiles
+constexpr int column_tiles() { return NT > 128 ? 2 : 1; }   // 128-row scale tiles of the columns
 template <int NT>
-constexpr int stage_bytes() { return kWTile + NT * kRowB + 2 * kSfTile * (1 + token_tiles<NT>()); }
+constexpr int stage_bytes() { return kWTile + NT * kRowB + 2 * kSfTile * (1 + column_tiles<NT>()); }
 template <int NT>
 constexpr int stages() {
     const int s = (220 * 1024) / stage_bytes<NT>();
     return s > 10 ? 10 : s;
 }
-// TMEM columns: NT of accumulator, then per stage 8 of weight scales and 8 per token tile.
+// TMEM columns: NT of accumulator, then per stage 8 of the lanes' scales and 8 per column tile.
 template <int NT>
-constexpr int sf_cols() { return 8 * (1 + token_tiles<NT>()); }
+constexpr int sf_cols() { return 8 * (1 + column_tiles<NT>()); }
 template <int NT>
 constexpr uint32_t tmem_cols() {
     const int c = NT + stages<NT>() * sf_cols<NT>();
@@ -90,21 +91,27 @@ __device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float
     else reinterpret_cast<float*>(out)[i] = v;
 }
 
-// grid (weight row tiles of RT, token tiles of NT)
+// ---- tokens on the columns -----------------------------------------------------------------
+// Grid (weight row tiles of RT, 1): a CTA keeps up to 10 stages in flight and has no second
+// tile.  Four epilogue warps: a thread holds one output feature and walks the tokens, the 32
+// lanes of a warp writing consecutive features.  An MMA of 128 lanes takes some 70 clocks however
+// few columns it has and a scale copy some 40, so at RT = 64 a stage's 8 KB of weights take about
+// 450 clocks: 8 tokens x 8192 x 2048 in 5.3 to 6.2 us, of which 3.2 are the launch and one stage
+// (8.9 MB: 1.4 us at the copy rate).
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b,
                       const __grid_constant__ CUtensorMap tmap_a, const GemmArgs g, const int RT) {
     using namespace sm100;
-    constexpr int S = stages<NT>(), kTT = token_tiles<NT>();
+    constexpr int S = stages<NT>();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
     uint8_t* sW = smem;                                  // [S][128 rows x 128 B]
     uint8_t* sX = sW + S * kWTile;                       // [S][NT rows x 128 B]
     uint8_t* sSw = sX + S * NT * kRowB;                  // [S][2][512]
-    uint8_t* sSx = sSw + S * 2 * kSfTile;                // [S][kTT][2][512]
-    uint64_t* full = reinterpret_cast<uint64_t*>(sSx + S * kTT * 2 * kSfTile);
+    uint8_t* sSx = sSw + S * 2 * kSfTile;                // [S][2][512]
+    uint64_t* full = reinterpret_cast<uint64_t*>(sSx + S * 2 * kSfTile);
     uint64_t* empty = full + S;
     uint64_t* accfull = empty + S;
     uint64_t* drain = accfull + 1;
@@ -177,22 +184,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t wd = smem_desc_k_sw128(sW + s * kWTile);
             const uint64_t xd = smem_desc_k_sw128(sX + s * NT * kRowB);
             const uint64_t swd = smem_desc_rows16(sSw + s * 2 * kSfTile);
-            const uint64_t sxd = smem_desc_rows16(sSx + s * kTT * 2 * kSfTile);
+            const uint64_t sxd = smem_desc_rows16(sSx + s * 2 * kSfTile);
             if (elect_one()) {
 #pragma unroll
                 for (int kt = 0; kt < 2; kt++)
                     if (128 * kt < kleft) {
                         tmem_cp_32x128b_x4(sfw + 4 * kt, swd + (kt * kSfTile >> 4));
-#pragma unroll
-                        for (int t = 0; t < kTT; t++)
-                            tmem_cp_32x128b_x4(sfx + 4 * (kt * kTT + t), sxd + ((t * 2 + kt) * kSfTile >> 4));
+                        tmem_cp_32x128b_x4(sfx + 4 * kt, sxd + (kt * kSfTile >> 4));
                     }
 #pragma unroll
                 for (int j = 0; j < 4; j++)
                     if (64 * j < kleft) {
                         const uint32_t id = 2 * (j & 1), sel = id << 30;
                         mma_mxf4(tmem, wd + 2 * j, xd + 2 * j, instr_desc_mxf4(128, NT, id, id),
-                                 (sfw + 4 * (j >> 1)) | sel, (sfx + 4 * kTT * (j >> 1)) | sel,
+                                 (sfw + 4 * (j >> 1)) | sel, (sfx + 4 * (j >> 1)) | sel,
                                  i > 0 || j > 0 ? 1u : 0u);
                     }
                 mma_commit(&empty[s]);
@@ -240,7 +245,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // that neighbours share the weight's rows in L2).  Eight epilogue warps, two per lane quarter,
 // take the accumulator into registers at once (CT / 2 columns a thread) and hand it back, so
 // the next tile's MMAs wait for those loads only; the conversion, a 2 KB transposition per warp
-// in shared memory and the stores of 64 contiguous bytes a row run beside them.
+// in shared memory and the stores of 64 contiguous bytes a row (TMA where rows allow) run beside
+// them.  8192 x 8192 x 2048 to bf16: 65 us, 4.2 PFLOP/s; without the stores 50, whose traffic
+// (134 MB) competes with the operands' loads; 5.5 PFLOP/s per further stage.  Tried and slower:
+// two accumulators of 192 columns (75 us), scales written to TMEM by four warps instead of
+// copies in the MMA warp's stream (71), streaming stores (69), features fastest (71).
 constexpr int kWideThreads = 320;
 constexpr int kStageRowB = 64;           // bytes of a row per transposition
 
@@ -278,7 +287,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                            const __grid_constant__ CUtensorMap tmap_out, const GemmArgs g, const int mtiles,
                            const int tiles, const int tma_out) {
     using namespace sm100;
-    constexpr int S = wide_stages<CT>(), kTT = token_tiles<CT>(), kAcc = wide_accs<CT>();
+    constexpr int S = wide_stages<CT>(), kTT = column_tiles<CT>(), kAcc = wide_accs<CT>();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));

@@ -147,7 +147,8 @@ def test_matmul_exact_sums_bit_exact(M, N, K, dt):
 
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("M,N,K,pad", [(70, 64, 256, 0), (129, 200, 96, 8), (300, 264, 2048, 16), (1, 8, 32, 8),
-                                       (257, 4104, 64, 0), (1000, 1112, 320, 24), (2000, 2560, 160, 0)])
+                                       (257, 4104, 64, 0), (1000, 1112, 320, 24), (2000, 2560, 160, 0),
+                                       (100, 8, 544, 8), (65, 24, 32, 0)])
 def test_matmul_aligned_rows_bit_exact(M, N, K, pad, dt):
     # rows of whole 16-byte pieces (the tiles are then stored by the TMA unit): nothing outside
     # the N columns is written, rows past M neither
