@@ -482,7 +482,9 @@ csa_status_t csa_mxfp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uint8
  * Arguments:
  *   q, k, q_out, k_out: [T, heads, D] in dtype, element strides *_st between tokens and *_sh
  *   between heads; q has H heads, k has Hk (either may be NULL with 0 heads).  An output may
- *   be its own input (same pointer and strides); otherwise outputs overlap nothing.
+ *   be its own input (same pointer and strides); otherwise outputs overlap nothing.  Output
+ *   rows that would overlap one another by their strides are refused; an input's may (an
+ *   expanded tensor).
  *   q_weight, k_weight: fp32 [D], nullable (ones), 16-byte aligned; pos int32 [T]
  *   D: a multiple of 8 up to 1024; rope_dims: even, 0 .. min(D, 128)
  *   (sparse_mqa_attn and dense_hca_attn rotate their queries themselves: rope_dims = 0 makes

@@ -564,6 +564,13 @@ static bool rows_aligned(const void* p, int64_t st, int64_t sh, int es) {
     return aligned(p, 16) && st * es % 16 == 0 && sh * es % 16 == 0;
 }
 
+// Whether [T, heads, D] rows at these strides lie apart from one another (outputs).
+static bool rows_disjoint(int64_t st, int64_t sh, int64_t T, int64_t heads, int64_t D) {
+    if (heads <= 1) return T <= 1 || st >= D;
+    if (T <= 1) return sh >= D;
+    return (sh >= D && st >= (heads - 1) * sh + D) || (st >= D && sh >= (T - 1) * st + D);
+}
+
 csa_status_t csa_qk_norm_rope(const void* q, int64_t q_st, int64_t q_sh, const void* k,
                               int64_t k_st, int64_t k_sh, const int32_t* pos,
                               const float* q_weight, const float* k_weight, void* q_out,
@@ -584,6 +591,9 @@ csa_status_t csa_qk_norm_rope(const void* q, int64_t q_st, int64_t q_sh, const v
     REQUIRE((H == 0 || (rows_aligned(q, q_st, q_sh, es) && rows_aligned(q_out, qo_st, qo_sh, es))) &&
                 (Hk == 0 || (rows_aligned(k, k_st, k_sh, es) && rows_aligned(k_out, ko_st, ko_sh, es))),
             "rows must be 16-byte aligned (pointers and strides)");
+    REQUIRE((H == 0 || rows_disjoint(qo_st, qo_sh, T, H, D)) &&
+                (Hk == 0 || rows_disjoint(ko_st, ko_sh, T, Hk, D)),
+            "output rows overlap (token and head strides)");
     SUPPORT((int64_t)T * (H + Hk) <= (1ll << 32), "too many rows");
     const csa::QkRows qr{q, q_out, q_weight, q_st, q_sh, qo_st, qo_sh, H};
     const csa::QkRows kr{k, k_out, k_weight, k_st, k_sh, ko_st, ko_sh, Hk};

@@ -507,3 +507,60 @@ def test_matmul_wait_timeout_is_reported_and_recovers(M, N, K):
     out = _matmul(a, b, "f32", st=st)
     _sync(st)
     assert np.array_equal(f64(out), a[2] @ b[2].T)
+
+
+def test_expanded_inputs_and_overlapping_outputs():
+    # one row read for every head and token; an expanded output is refused
+    x = torch.randn((1, 1, 128), device=DEV)
+    pos = torch.arange(5, dtype=torch.int32, device=DEV)
+    y = torch.empty((5, 3, 128), device=DEV)
+    L.csa_qk_norm_rope(x.expand(5, 3, 128), None, pos, y, None)
+    ref = io.norm_rope(f64(x.expand(5, 3, 128)), np.arange(5))
+    torch.cuda.synchronize()
+    assert np.abs(f64(y) - ref).max() < 1e-5
+    with pytest.raises(L.CSAError, match="overlap"):
+        L.csa_qk_norm_rope(y, None, pos, x.expand(5, 3, 128), None)
+    codes, scale = _store(L.CSA_IDX_FP8, (5, 3), 128)
+    L.csa_indexer_queries(x.expand(5, 3, 128), pos, codes, scale)
+    torch.cuda.synchronize()
+    _same(codes, scale, io.fp8(ref))
+
+
+def test_offsets_past_32_bits():
+    # quantised rows, a product's result and a key store whose last rows lie past 2^32 bytes (and
+    # past 2^31 elements)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    rows, cols = (1 << 26) + 40, 64
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device=DEV)
+    x[-70:] = torch.randn((70, cols), generator=g, device=DEV).to(torch.bfloat16)
+    codes, sf = torch.full((rows, cols // 2), 9, dtype=torch.uint8, device=DEV), _sf_empty(rows, cols, 0)
+    L.csa_mxfp4_quantize(x, codes, sf)
+    p, s = io.mxfp4(f64(x[-70:]))
+    assert np.array_equal(codes[-70:].cpu().numpy(), p) and np.array_equal(sf[-70:].cpu().numpy(), s)
+    assert int(codes[:-70].max()) == 0 and int(sf[:-70].max()) == 0
+    x.fill_(7.0)
+    L.csa_mxfp4_dequantize(codes, sf, x)
+    assert np.array_equal(f64(x[-70:]), io.mxfp4_values(p, s)) and float(x[:-70].abs().max()) == 0
+    del x, codes, sf
+    rng = np.random.default_rng(4)
+    M, N, K = 70001, 32768, 32
+    a, b = _operands(rng, M, N, K, 126, 127)
+    out = _matmul(a, b, "bf16")
+    for r in (0, 65536, 65537, M - 1):
+        want = torch.from_numpy(a[2][r:r + 1] @ b[2].T).to(torch.bfloat16)
+        assert torch.equal(out[r:r + 1].cpu(), want), r
+    del out
+    ent_rows = (1 << 25) + 64
+    for fmt in (L.CSA_IDX_FP8, L.CSA_IDX_MXFP4):
+        codes, scale = _store(fmt, (ent_rows,), 128)
+        k = torch.randn((3, 128), generator=g, device=DEV)
+        table = torch.tensor([[5, (1 << 20) + 1]], dtype=torch.int32, device=DEV)
+        i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+        st = _status()
+        L.csa_indexer_append(k, torch.tensor([250], device=DEV), None, i32(0, 0, 0), i32(3, 40, 61), codes, scale,
+                             B=1, fmt=fmt, layout=L.cache_layout(table), dev_status=st)
+        _sync(st)
+        at = torch.tensor([5 * 32 + 3, (1 << 25) + 32 + 8, (1 << 25) + 32 + 29], device=DEV)
+        y = io.norm_rope(f64(k)[:, None], np.array([15, 163, 247]))[:, 0]
+        _same(codes[at], scale[at], _quant_ref(y, fmt))
+        del codes, scale

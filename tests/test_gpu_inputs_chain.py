@@ -220,3 +220,45 @@ def test_projection_and_cache_refuse_what_they_cannot_hold():
     z = torch.zeros((1, 128), dtype=torch.bfloat16, device=DEV)
     with pytest.raises(ValueError, match="append_keys"):
         hc.append(z, z, z.to(torch.uint8), torch.zeros(1, device=DEV))
+
+
+def test_normed_queries_go_straight_into_the_attention():
+    """csa_qk_norm_rope directly before the attention that reads its rows ahead of its own wait:
+    back to back on changing inputs, against synchronised calls."""
+    g = torch.Generator(device=DEV).manual_seed(29)
+    B, T, k = 4, 3000, 64
+    kv = torch.randn((B * T, D), generator=g, device=DEV).to(torch.bfloat16)
+    ents = torch.randn((B * T // 4, D), generator=g, device=DEV).to(torch.bfloat16).view(torch.uint8)
+    i64 = lambda v: torch.tensor(v, dtype=torch.int64, device=DEV)  # noqa: E731
+    seq_len, off, kvo, p0 = i64([T] * B), i64([b * (T // 4) for b in range(B)]), i64([b * T for b in range(B)]), i64([0] * B)
+    q_seq = torch.arange(B, dtype=torch.int32, device=DEV)
+    q_pos = torch.full((B,), T - 1, dtype=torch.int32, device=DEV)
+    idx = torch.stack([torch.randperm(T // 4, generator=g, device=DEV)[:k].sort().values for _ in range(B)]).to(torch.int32)
+    sink = torch.randn(H, generator=g, device=DEV)
+    w = 1 + 0.2 * torch.randn(D, generator=g, device=DEV)
+    data = [torch.randn((B, H, D), generator=g, device=DEV).to(torch.bfloat16) for _ in range(5)]
+    q, qn = torch.empty_like(data[0]), torch.empty_like(data[0])
+    out = torch.empty_like(q)
+
+    def step(sync):
+        L.csa_qk_norm_rope(q, None, q_pos, qn, None, q_weight=w, rope_dims=0)
+        if sync:
+            torch.cuda.synchronize()
+        L.sparse_mqa_attn(qn, ents, seq_len, off, kv, kvo, p0, q_seq, q_pos, idx, sink, out, fmt=0, B=B, H=H, D=D,
+                          W=128, m=4, k=k, softmax_scale=D ** -0.5)
+
+    want, got = [], []
+    for r in range(5):
+        q.copy_(data[r])
+        step(True)
+        want.append(out.clone())
+    for r in range(20):
+        q.copy_(data[r % 5])
+        step(False)
+        got.append(out.clone())
+    for r in range(20):              # and without a copy in between: the previous attention still runs
+        step(False)
+    torch.cuda.synchronize()
+    for r in range(20):
+        assert torch.equal(got[r], want[r % 5]), r
+    assert torch.equal(out, want[19 % 5])

@@ -119,8 +119,8 @@ def test_matmul_refusals(args, status, text):
 
 
 def _qk(q=F, st=256, sh=128, k=F, pos=F, qw=None, qo=F, ko=F, dt=0, T=2, H=2, Hk=1, D=128,
-        rope=64, norm=1, theta=1e4, eps=1e-6):
-    return lib.csa_qk_norm_rope(q, st, sh, k, 128, 128, pos, qw, None, qo, 256, 128, ko, 128, 128,
+        rope=64, norm=1, theta=1e4, eps=1e-6, ost=256, osh=128, kst=128):
+    return lib.csa_qk_norm_rope(q, st, sh, k, 128, 128, pos, qw, None, qo, ost, osh, ko, kst, 128,
                                 dt, T, H, Hk, D, rope, norm, theta, eps, None)
 
 
@@ -132,7 +132,9 @@ def _qk(q=F, st=256, sh=128, k=F, pos=F, qw=None, qo=F, ko=F, dt=0, T=2, H=2, Hk
     (dict(ko=None), 1, "null"), (dict(pos=None), 1, "null"), (dict(q=ODD), 1, "aligned"),
     (dict(sh=130), 1, "aligned"), (dict(st=100), 1, "aligned"), (dict(T=-1), 1, ">= 0"),
     (dict(Hk=-1), 1, ">= 0"), (dict(dt=4), 1, "element type"),
-    (dict(theta=float("nan")), 1, "theta"), (dict(H=(1 << 20) + 1), 2, "heads")])
+    (dict(theta=float("nan")), 1, "theta"), (dict(H=(1 << 20) + 1), 2, "heads"),
+    (dict(osh=0), 1, "overlap"), (dict(ost=128), 1, "overlap"), (dict(ost=0), 1, "overlap"),
+    (dict(osh=64), 1, "overlap"), (dict(kst=64), 1, "overlap"), (dict(ost=-256), 1, "overlap")])
 def test_qk_norm_rope_refusals(kw, status, text):
     assert _qk(**kw) == status and text in _err()
 
