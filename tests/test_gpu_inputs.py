@@ -564,3 +564,68 @@ def test_offsets_past_32_bits():
         y = io.norm_rope(f64(k)[:, None], np.array([15, 163, 247]))[:, 0]
         _same(codes[at], scale[at], _quant_ref(y, fmt))
         del codes, scale
+
+
+@pytest.mark.parametrize("M,N,K,fill", [(5, 70, 256, 255), (300, 70, 256, 255), (5, 70, 96, 254), (300, 515, 96, 254),
+                                        (300, 1, 64, 255), (65, 2, 32, 254)])
+def test_matmul_padding_scales_do_not_matter(M, N, K, fill):
+    # scale tiles whose padding was never written: of rows anything (K fills its tiles), of
+    # blocks past K anything finite
+    rng = np.random.default_rng(K + fill)
+    a, b = _operands(rng, M, N, K, 126, 127)
+    if fill == 255 and K % 128:
+        fill = 254
+    out = _matmul(a, b, "f32", fill=fill)
+    torch.cuda.synchronize()
+    assert np.array_equal(f64(out), a[2] @ b[2].T)
+
+
+def test_misaligned_views_are_refused():
+    u8 = lambda *n: torch.zeros(n, dtype=torch.uint8, device=DEV)  # noqa: E731
+    x = torch.zeros((8, 256), dtype=torch.bfloat16, device=DEV)
+    L.csa_mxfp4_quantize(x[:, 8:136], u8(8, 64), u8(8, 4))
+    with pytest.raises(L.CSAError, match="aligned"):
+        L.csa_mxfp4_quantize(x[:, 4:132], u8(8, 64), u8(8, 4))
+    with pytest.raises(L.CSAError, match="multiple of 16 bytes"):
+        L.csa_mxfp4_quantize(torch.zeros((8, 132), dtype=torch.bfloat16, device=DEV)[:, :128], u8(8, 64), u8(8, 4))
+    q = torch.zeros((2, 4, 132), dtype=torch.bfloat16, device=DEV)[..., :128]
+    pos = torch.zeros(2, dtype=torch.int32, device=DEV)
+    with pytest.raises(L.CSAError, match="aligned"):
+        L.csa_indexer_queries(q, pos, u8(2, 4, 128), torch.zeros((2, 4), device=DEV))
+    with pytest.raises(L.CSAError, match="contiguous along|contiguous channels"):
+        L.csa_qk_norm_rope(x.unflatten(1, (128, 2)).transpose(1, 2), None, torch.zeros(8, dtype=torch.int32, device=DEV),
+                           torch.zeros((8, 2, 128), dtype=torch.bfloat16, device=DEV), None)
+
+
+def test_two_threads_on_two_streams():
+    import threading
+    rng = np.random.default_rng(12)
+    jobs = []
+    for M, N, K in ((40, 1000, 512), (700, 520, 512)):
+        a, b = _operands(rng, M, N, K, 126, 127)
+        dev = [_gpu(v) for v in (a[0], io.tile_scales(a[1]), b[0], io.tile_scales(b[1]))]
+        jobs.append((dev, torch.zeros((M, N), device=DEV), a[2] @ b[2].T, torch.cuda.Stream(), []))
+    torch.cuda.synchronize()
+
+    def work(dev, out, want, stream, errors):
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(50):
+                    L.csa_mxfp4_matmul(*dev, out)
+                try:
+                    L.csa_mxfp4_matmul(*dev[:3], dev[3][:16], out)
+                    errors.append("not refused")
+                except L.CSAError as e:
+                    if "b's scales" not in str(e):
+                        errors.append(str(e))
+        except Exception as e:      # noqa: BLE001  (reported by the main thread)
+            errors.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for _, out, want, _, errors in jobs:
+        assert not errors and np.array_equal(f64(out), want)
