@@ -10,8 +10,8 @@
 // the whole row stays in registers between its one load and its one store; a warp walks rows
 // (heads) that share a position, whose cosines and sines its lanes form once, in fp64, a pair
 // each.  8192 tokens of 64 + 1 heads x 128 in bf16 (273 MB): norm and rotation 50 us, 5.4 TB/s,
-// bound by HBM; query heads to MXFP4 (170 MB) 48 to 56 us, bound by instructions (256 per lane
-// and 16 channels, half of them the scale, the brackets and the codes).
+// bound by HBM; query heads to MXFP4 (170 MB) 50 us, to FP8 (203 MB) 68, bound by instructions
+// (256 per lane and 16 channels for MXFP4, half of them the scale, the brackets and the codes).
 #include "launchers.cuh"
 #include "rows.cuh"
 
@@ -180,27 +180,26 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const QkArgs 
 // The codes are those of the definition, whatever the order of the sums: an e4m3 or e2m1 code
 // (or a block's power-of-two scale) next to a rounding border is not left to fp32.  The fast
 // path computes in fp32 and brackets every quotient z by its error bound: if the codes of z -
-// margin and z + margin agree, that code is the one.  If they differ anywhere in the warp's
-// rows (about 1 pass in 200 on normal data), or the values leave the range the bound holds in,
-// the rows are done again in fp64.
+// margin and z + margin agree, that code is the one.  If they differ anywhere in the warp's rows,
+// or the values leave the range the bound holds in, the rows are done again in fp64.
 //
 // v = x * weight, rotated, is left without the norm's factor r, which joins the scale.  The
-// bound, u = 2^-24, relative to |v1| + |v2| of a rotated pair before the rotation (|v|
-// elsewhere): the product with the weight, cos or sin, the product with it, the sum: 4 u.
+// bound, u = 2^-24: v is off by 4 u of |v1| + |v2| of its pair before the rotation, or of |v|
+// without one (the product with the weight, cos or sin, the product with it, the sum); the rest
+// is relative to z:
 //   MXFP4: z = v * (r * 2^-e).  The sum of squares takes at most 6 roundings in a lane and
 //   log2(LPR) <= 3 across, the mean and eps 1, of which rsqrt halves 5 u and adds its
-//   2 ulp = 4 u; the product u, the bracket u: 15 u.  (|v1| + |v2| <= 2 max|v|, since a
-//   rotation keeps the pair's length: 30 u bound the block's largest.)
-//   e4m3: z = v * (448 / max|v|), from which r drops out: 4 u, twice 4 u of the largest |v|, u
-//   each of the division, the product, the definition's rounding of the scale to fp32 and the
-//   bracket: 16 u.
-// With rows' sums of squares
-// below 2^100, weights below 2^40 and results within 2^-60 .. 2^100 nothing overflows, and an
-// underflowed product is below 2^-34 of a quotient's unit, far from every border but zero's,
-// whose sign it keeps.
+//   2 ulp = 4 u; the product u: 10 u.  The block's largest |v| is off by 8 u of itself (|v1| +
+//   |v2| <= 2 max|v|, since a rotation keeps the pair's length), and 10 u with r.
+//   e4m3: z = v * (448 / max|v|), from which r drops out: 8 u of the largest |v|, u each of the
+//   division, the product, the definition's rounding of the scale to fp32: 11 u.
+// The bracket's own roundings add 2 u.  Counted whole against |v1| + |v2|, the bound of e4m3, whose
+// codes are dense near zero, sent 1 pass in 15 to fp64, where this sends 1 in 38 (8192 tokens of
+// 64 x 128: 72 -> 68 us; MXFP4 sends 1 in 200 either way).  With rows' sums of squares below 2^100, weights below 2^40 and results within 2^-60 .. 2^100 nothing
+// overflows, and an underflowed product is below 2^-34 of a quotient's unit, far from every
+// border but zero's, whose sign it keeps.
 constexpr float kU24 = 5.9604645e-08f;
-constexpr float kFp4Margin = 20.f * kU24;
-constexpr float kFp8Margin = 20.f * kU24;
+constexpr float kAbsMargin = 5.f * kU24, kRelMargin = 15.f * kU24, kTopMargin = 24.f * kU24;
 constexpr float kTiny = 8.6736174e-19f, kHuge = 1.2676506e+30f;   // 2^-60, 2^100
 
 struct RowQuant {
@@ -347,12 +346,14 @@ struct LaneParams {
     __device__ __forceinline__ const double2* rot(int c) const { return rotated(c) ? table->f64 + pair[c] : nullptr; }
 };
 
-// The brackets of a chunk's quotients v * inv: eps * |v * inv| to each side, or for a rotated
-// chunk eps * (mag of the pair) * inv.
-__device__ __forceinline__ void bracket(const float* v, const float* mag, bool rotated, float inv, float eps,
-                                        float* lo, float* hi) {
-    if (rotated) {
-        const float inv2[2] = {inv, inv}, m = eps * inv;
+// The brackets of a chunk's quotients z = v * inv: kAbsMargin times the pair's magnitude before the
+// rotation (scaled alike) plus kRelMargin |z| to each side, or without a rotation both times |z|;
+// for e2m1, whose codes are few, both times the pair's magnitude (cheaper: 50 us against 51).
+template <bool FP4>
+__device__ __forceinline__ void bracket(const float* v, const float* mag, bool rotated, float inv, float* lo,
+                                        float* hi) {
+    if (FP4 && rotated) {
+        const float inv2[2] = {inv, inv}, m = (kAbsMargin + kRelMargin) * inv;
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             const float d = mag[i] * m, down[2] = {-d, -d}, up[2] = {d, d};
@@ -361,7 +362,20 @@ __device__ __forceinline__ void bracket(const float* v, const float* mag, bool r
             add2(lo + 2 * i, z, down);
             add2(hi + 2 * i, z, up);
         }
+    } else if (rotated) {
+        const float inv2[2] = {inv, inv}, m = kAbsMargin * inv;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            float z[2];
+            mul2(z, v + 2 * i, inv2);
+            const float d = mag[i] * m;
+            const float up[2] = {fmaf(fabsf(z[0]), kRelMargin, d), fmaf(fabsf(z[1]), kRelMargin, d)};
+            add2(hi + 2 * i, z, up);
+            lo[2 * i] = z[0] - up[0];
+            lo[2 * i + 1] = z[1] - up[1];
+        }
     } else {
+        constexpr float eps = kAbsMargin + kRelMargin;
         const float a = fmaf(inv, -eps, inv), b = fmaf(inv, eps, inv), a2[2] = {a, a}, b2[2] = {b, b};
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
@@ -423,7 +437,7 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
             const float top = amax[c] * r;
             const uint32_t ex = __float_as_uint(top) >> 23;
             // the largest magnitude may itself lie next to a power of two
-            const float above = fmaf(top, 2.1f * kFp4Margin, top), below = fmaf(top, -2.1f * kFp4Margin, top);
+            const float above = fmaf(top, kTopMargin, top), below = fmaf(top, -kTopMargin, top);
             near |= !zero & (!(fminf(amax[c], top) > kTiny) | !(top < kHuge) |
                              ((__float_as_uint(above) ^ __float_as_uint(below)) >> 23 != 0u));
             // a non-finite block is `near`: the bounds only keep the shift in range
@@ -432,7 +446,7 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
             q.bad[c] = false;
             const float inv = zero ? 1.f : r * __uint_as_float((254u - e) << 23);     // r * 2^(127 - e)
             float lo[8], hi[8];
-            bracket(v.v[c], mag[c], p.rotated(c), inv, kFp4Margin, lo, hi);
+            bracket<true>(v.v[c], mag[c], p.rotated(c), inv, lo, hi);
             q.c[c][0] = pack_e2m1x8(lo);
             q.c[c][1] = 0;
             near |= !zero & (pack_e2m1x8(hi) != q.c[c][0]);     // zeros keep their sign in lo
@@ -447,7 +461,7 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
 #pragma unroll
         for (int c = 0; c < kC; c++) {
             float lo[8], hi[8];
-            bracket(v.v[c], mag[c], p.rotated(c), inv, kFp8Margin, lo, hi);
+            bracket<false>(v.v[c], mag[c], p.rotated(c), inv, lo, hi);
             const uint2 a = pack_e4m3x8(lo), b = pack_e4m3x8(hi);
             q.c[c][0] = a.x;
             q.c[c][1] = a.y;
