@@ -318,9 +318,10 @@ def dense_hca_attn(q, entries, seq_len, ent_off, kv, kv_off, kv_pos0, q_seq, q_p
 
 # ---- the lightning indexer's inputs --------------------------------------------------
 # These calls check their tensors' types, shapes and devices, since a wrong one would be
-# read past its end; sizes and alignments are checked by the library.  Each call tests all
-# of it in one expression of cheap accessors (decode steps issue many small launches, and
-# the host time per call is what bounds them); only a failed test looks for the reason.
+# read past its end; sizes and alignments are checked by the library.  Decode steps issue many
+# small launches, and the host time per call is what bounds them: the tests and the
+# conversion of the arguments are compiled (csrc/marshal.cpp).  Where a test fails, or that
+# module was not built, the call below does the same in Python, finds the reason and raises.
 _DTYPES = {torch.bfloat16: CSA_DT_BF16, torch.float16: CSA_DT_F16, torch.float32: CSA_DT_F32}
 _U8, _I32T, _I64T, _F32T = torch.uint8, torch.int32, torch.int64, torch.float32
 # The current stream's handle without a Stream object (3 us less per call) and the current
@@ -332,6 +333,18 @@ _mx_quantize, _mx_dequantize, _mx_matmul = (_lib.csa_mxfp4_quantize, _lib.csa_mx
                                             _lib.csa_mxfp4_matmul)
 _qk_norm_rope, _idx_queries, _idx_append = (_lib.csa_qk_norm_rope, _lib.csa_indexer_queries,
                                             _lib.csa_indexer_append)
+
+
+try:
+    from . import _csa_marshal as _marshal
+    _marshal.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        _mx_quantize, _mx_dequantize, _mx_matmul, _qk_norm_rope, _idx_queries, _idx_append)))
+except ImportError:
+    _marshal = None
+
+
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def _bad(message: str):
@@ -431,6 +444,12 @@ def csa_mxfp4_quantize(x, codes, sf, *, sf_layout: int = CSA_SF_ROWS, dev_status
                        stream=None):
     """Rows of x (bf16, fp16 or fp32 [rows, cols], any row stride) to packed e2m1 codes and
     UE8M0 scales in blocks of 32 (see include/csa.h)."""
+    if _marshal is not None:
+        status = _marshal.quantize(x, codes, sf, sf_layout, dev_status, _handle(stream))
+        if status == 0:
+            return
+        if status is not None:
+            _check(status)
     dev, dtype = x.get_device(), _DTYPES.get(x.dtype)
     if x.dim() != 2:
         _need_2d(x, "x")
@@ -450,6 +469,12 @@ def csa_mxfp4_quantize(x, codes, sf, *, sf_layout: int = CSA_SF_ROWS, dev_status
 
 def csa_mxfp4_dequantize(codes, sf, out, *, sf_layout: int = CSA_SF_ROWS, stream=None):
     """The values MXFP4 rows stand for, into out (bf16, fp16 or fp32 [rows, cols])."""
+    if _marshal is not None:
+        status = _marshal.dequantize(codes, sf, out, sf_layout, _handle(stream))
+        if status == 0:
+            return
+        if status is not None:
+            _check(status)
     dev, dtype = out.get_device(), _DTYPES.get(out.dtype)
     if out.dim() != 2:
         _need_2d(out, "out")
@@ -468,6 +493,12 @@ def csa_mxfp4_dequantize(codes, sf, out, *, sf_layout: int = CSA_SF_ROWS, stream
 def csa_mxfp4_matmul(a, a_sf, b, b_sf, out, *, dev_status=None, stream=None):
     """out[m, n] = sum_k A[m, k] B[n, k] of packed MXFP4 a [M, K / 2] and b [N, K / 2] with
     tiled scales (CSA_SF_TILED), out bf16, fp16 or fp32 [M, N] (any row stride)."""
+    if _marshal is not None:
+        status = _marshal.matmul(a, a_sf, b, b_sf, out, dev_status, _handle(stream))
+        if status == 0:
+            return
+        if status is not None:
+            _check(status)
     dev, dtype = out.get_device(), _DTYPES.get(out.dtype)
     if out.dim() != 2:
         _need_2d(out, "out")
@@ -530,6 +561,13 @@ def csa_qk_norm_rope(q, k, pos, q_out, k_out, *, q_weight=None, k_weight=None, n
     """RMSNorm of the query heads q [T, H, D] and key heads k [T, Hk, D] (either may be None)
     and rotation of their last rope_dims channels at pos (int32 [T]), in one launch.  An
     output may be its own input."""
+    if _marshal is not None:
+        status = _marshal.qk_norm_rope(q, k, pos, q_out, k_out, q_weight, k_weight, norm, rope_dims,
+                                       rope_theta, eps, _handle(stream))
+        if status == 0:
+            return
+        if status is not None:
+            _check(status)
     lead = q if q is not None else k
     if lead is None:
         _bad("q and k are both None")
@@ -591,6 +629,13 @@ def csa_indexer_queries(q, q_pos, codes, scale, *, fmt: int = CSA_IDX_FP8, weigh
     """The indexer's query heads q [Q, H, D] normed, rotated at q_pos and quantised: codes and
     scale are lightning_indexer_topk's qI and qI_scale (fmt CSA_IDX_FP8) or
     lightning_indexer_topk_mxfp4's qI and qI_sf (CSA_IDX_MXFP4)."""
+    if _marshal is not None:
+        status = _marshal.queries(q, q_pos, codes, scale, fmt, weight, norm, rope_dims, rope_theta,
+                                  eps, dev_status, _handle(stream))
+        if status == 0:
+            return
+        if status is not None:
+            _check(status)
     if q.dim() != 3:
         _bad(f"q must be [Q, H, D], not {tuple(q.shape)}")
     Q, H, D = q.shape
@@ -622,8 +667,18 @@ def csa_indexer_append(k, seq_len, ent_off, item_seq, item_ent, codes, scale, *,
     """Indexer keys k [n, D] of the listed entries normed, rotated at their block ends,
     quantised and written to their rows of the key store (codes, scale), through the layout's
     block table or ent_off."""
+    bt, ring = None, 0
+    if layout is not None:
+        bt, ring = getattr(layout, "_block_table", None), layout.kv_ring
+    if _marshal is not None and (bt is not None or layout is None or not layout.block_table):
+        status = _marshal.append(k, seq_len, ent_off, item_seq, item_ent, codes, scale, B, m, fmt,
+                                 weight, norm, rope_dims, rope_theta, eps, bt, ring, dev_status,
+                                 _handle(stream))
+        if status == 0:
+            return
+        if status is not None:
+            _check(status)
     dev, dtype = k.get_device(), _DTYPES.get(k.dtype)
-    bt = None if layout is None else getattr(layout, "_block_table", None)
     if k.dim() != 2:
         _need_2d(k, "k")
     n, D = k.shape

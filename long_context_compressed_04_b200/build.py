@@ -2,7 +2,9 @@
 
 Each .cu file under csrc/ compiles to an object in parallel; the objects link into
 long_context_compressed_04_b200/libcsa.so with the CUDA runtime linked statically, so the
-library needs no CUDA shared library besides the driver at run time.
+library needs no CUDA shared library besides the driver at run time.  csrc/marshal.cpp, the
+Python binding's compiled argument marshalling, builds beside it with the host compiler
+against the installed torch (_csa_marshal.so).
 """
 from __future__ import annotations
 
@@ -17,6 +19,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libcsa.so")
+MARSHAL = os.path.join(HERE, "_csa_marshal.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -45,11 +48,36 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_marshal(force: bool = False) -> str:
+    import sysconfig
+
+    import torch
+    src = os.path.join(CSRC, "marshal.cpp")
+    if not (force or _stale(MARSHAL, [src, os.path.join(ROOT, "include", "csa.h")])):
+        return MARSHAL
+    troot = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-shared", "-fPIC",
+           "-std=c++17", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(troot, "include"),
+           "-isystem", os.path.join(troot, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), src, "-o", tmp,
+           "-L" + os.path.join(troot, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("build of _csa_marshal.so failed")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     srcs = _sources()
     hdrs = _headers()
     os.makedirs(OBJ_DIR, exist_ok=True)
     cc = nvcc()
+    marshal = concurrent.futures.ThreadPoolExecutor(max_workers=1).submit(build_marshal, force)
     jobs = []
     for s in srcs:
         obj = os.path.join(OBJ_DIR, os.path.basename(s)[:-3] + ".o")
@@ -76,6 +104,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link of libcsa.so failed")
         os.replace(tmp, OUT)
+    marshal.result()
     return OUT
 
 

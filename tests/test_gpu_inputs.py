@@ -629,3 +629,70 @@ def test_two_threads_on_two_streams():
     torch.cuda.synchronize()
     for _, out, want, _, errors in jobs:
         assert not errors and np.array_equal(f64(out), want)
+
+
+def test_compiled_and_python_marshalling_agree(monkeypatch):
+    # the same calls through csrc/marshal.cpp and through ctypes, bit for bit, with every optional
+    # argument; and both refuse alike
+    assert L._marshal is not None, "build the package: _csa_marshal.so is missing"
+    g = torch.Generator(device=DEV).manual_seed(41)
+    T, H, D = 6, 5, 128
+    x = torch.randn((T, H * D + 64), generator=g, device=DEV).to(torch.bfloat16)
+    q, k = x[:, :H * D].unflatten(1, (H, D)), torch.randn((T, 1, D), generator=g, device=DEV).to(torch.bfloat16)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device=DEV, dtype=torch.int32)
+    w, w2 = (1 + 0.2 * torch.randn(D, generator=g, device=DEV) for _ in range(2))
+    table = torch.randperm(8, generator=g, device=DEV).to(torch.int32).view(2, 4)
+    seq = torch.tensor([0, 1, 1, 0, 1, 0], dtype=torch.int32, device=DEV)
+    ent = torch.tensor([3, 100, 7, 64, 90, 0], dtype=torch.int32, device=DEV)
+    seq_len, off = torch.tensor([500, 450], device=DEV), torch.tensor([0, 128], device=DEV)
+    stream = torch.cuda.Stream()
+
+    def run(s):
+        out, st = [], _status()
+        u8 = lambda *n: torch.zeros(n, dtype=torch.uint8, device=DEV)  # noqa: E731
+        for lay in (L.CSA_SF_ROWS, L.CSA_SF_TILED):
+            codes, sf = u8(T, H * D // 2), u8(L.csa_mxfp4_sf_bytes(T, H * D, lay))
+            back = torch.zeros((T, H * D + 8), device=DEV)[:, :H * D]
+            L.csa_mxfp4_quantize(x[:, :H * D], codes, sf, sf_layout=lay, dev_status=st, stream=s)
+            L.csa_mxfp4_dequantize(codes, sf, back, sf_layout=lay, stream=s)
+            out += [codes, sf, back]
+        prod = torch.zeros((T, T + 3), dtype=torch.float16, device=DEV)
+        L.csa_mxfp4_matmul(codes, sf, codes, sf, prod[:, :T], dev_status=st, stream=s)
+        qo, ko = torch.zeros_like(q), torch.zeros_like(k)
+        L.csa_qk_norm_rope(q, k, pos, qo, ko, q_weight=w, k_weight=w2, rope_dims=32, rope_theta=500.0, eps=1e-5, stream=s)
+        k2 = torch.zeros_like(k)
+        L.csa_qk_norm_rope(None, k, pos, None, k2, norm=False, stream=s)
+        out += [prod, qo, ko, k2]
+        for fmt in (L.CSA_IDX_FP8, L.CSA_IDX_MXFP4):
+            codes, scale = _store(fmt, (T, H), D)
+            L.csa_indexer_queries(q, pos, codes, scale, fmt=fmt, weight=w, norm=False, rope_dims=32, rope_theta=500.0,
+                                  eps=1e-5, dev_status=st, stream=s)
+            kc, ks = _store(fmt, (256,), D)
+            for kw in (dict(layout=L.cache_layout(table)), dict(layout=None)):
+                L.csa_indexer_append(k[:, 0], seq_len, off, seq, ent, kc, ks, B=2, m=4, fmt=fmt, weight=w2, rope_dims=32,
+                                     rope_theta=500.0, eps=1e-5, dev_status=st, stream=s, **kw)
+            out += [codes, scale, kc, ks]
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        errors = []
+        for bad in (lambda: L.csa_mxfp4_quantize(x[:, :48], u8(T, 24), u8(T, 2)),
+                    lambda: L.csa_mxfp4_quantize(x[:, :64], u8(T, 32), u8(T, 2), sf_layout=5),
+                    lambda: L.csa_mxfp4_matmul(u8(4, 32), u8(8), u8(8, 32), u8(512), prod),
+                    lambda: L.csa_qk_norm_rope(q, k, pos.long(), qo, ko),
+                    lambda: L.csa_qk_norm_rope(q, None, pos, qo, None, rope_dims=63),
+                    lambda: L.csa_indexer_queries(q, pos, kc, ks),
+                    lambda: L.csa_indexer_append(k[:, 0], seq_len, None, seq, ent, u8(4, D), torch.zeros(4, device=DEV), B=2)):
+            with pytest.raises(L.CSAError) as e:
+                bad()
+            errors.append(str(e.value))
+        return out, errors
+
+    for s in (None, stream):
+        torch.cuda.synchronize()
+        fast = run(s)
+        with monkeypatch.context() as mp:
+            mp.setattr(L, "_marshal", None)
+            slow = run(s)
+        assert fast[1] == slow[1]
+        for a, b in zip(fast[0], slow[0]):
+            assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
