@@ -160,6 +160,10 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_kernel(
     const T* __restrict__ x, int64_t rows, uint32_t units, int64_t ld, const Tasks tk,
     uint32_t* __restrict__ codes, uint8_t* __restrict__ sf, const ScaleMap sm, int32_t* __restrict__ st) {
     pdl_wait();
+    // Rows in the tiled layout are read by the product and the inverse alone, which wait for this
+    // grid before they read anything: the next kernel may start.  Rows in the indexer's layout
+    // may be read ahead of that wait, so it may not.
+    if (sm.tiled) pdl_trigger();
     const int lane = threadIdx.x & 31;
     const int rstep = tk.row_step();
     const uint32_t ustep = tk.unit_step();
