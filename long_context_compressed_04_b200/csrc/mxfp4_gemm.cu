@@ -4,9 +4,9 @@
 //
 // Two kernels, one structure: a decode step's few tokens lie on the accumulator's columns and the
 // weight's rows on its 128 lanes, so that the weight streams 128 (or RT) rows at a time; a
-// larger batch has its tokens on the lanes and 64 to 256 weight rows on the columns.  In both a
-// result is summed over K ascending, K = 64 an instruction, so that its bits do not
-// depend on the batch (tested over both kernels and every tile width).
+// batch of more than 96 has its tokens on the lanes and 64 to 256 weight rows on the columns.
+// In both a result is summed over K ascending, K = 64 an instruction, so that its bits do
+// not depend on the batch (tested over both kernels and every tile width).
 //
 //   warp 0         TMA producer: per stage of K = 256 the rows of both operands (128 bytes
 //                  each, 128-byte swizzle) and their scale tiles (bulk copies: the tiled
@@ -85,19 +85,18 @@ struct GemmArgs {
     int kt128;        // scale tiles along K
 };
 
-__device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float v) {
-    if (dtype == CSA_DT_BF16) reinterpret_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
-    else if (dtype == CSA_DT_F16) reinterpret_cast<__half*>(out)[i] = __float2half_rn(v);
-    else reinterpret_cast<float*>(out)[i] = v;
-}
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
 
 // ---- tokens on the columns -----------------------------------------------------------------
-// Grid (weight row tiles of RT, 1): a CTA keeps up to 10 stages in flight and has no second
+// One CTA per RT weight rows (NT >= M): it keeps up to 10 stages in flight and has no second
 // tile.  Four epilogue warps: a thread holds one output feature and walks the tokens, the 32
-// lanes of a warp writing consecutive features.  An MMA of 128 lanes takes some 70 clocks however
-// few columns it has and a scale copy some 40, so at RT = 64 a stage's 8 KB of weights take about
-// 450 clocks: 8 tokens x 8192 x 2048 in 5.3 to 6.2 us, of which 3.2 are the launch and one stage
-// (8.9 MB: 1.4 us at the copy rate).
+// lanes of a warp writing consecutive features (the type chosen outside the walk and one running
+// pointer: 64 tokens 7.1 -> 5.6 us).  An MMA of 128 lanes takes some 70 clocks however few
+// columns it has and a scale copy some 40, so at RT = 64 a stage's 8 KB of weights take about
+// 450 clocks: 8 tokens x 8192 x 2048 in 5.3 us, of which 3.2 are the launch and one stage (8.9 MB:
+// 1.4 us at the copy rate).
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b,
@@ -119,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_smem + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n0 = blockIdx.x * RT, m0 = blockIdx.y * NT;
+    const int n0 = blockIdx.x * RT;
     const int row0 = n0 & 127;                // the tile's first lane: its place in its scale tile
     const int nk = (g.K + kStageK - 1) / kStageK;
     if (threadIdx.x == 0) {
@@ -146,7 +145,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         const uint8_t* bsf = g.b_sf + (int64_t)(n0 >> 7) * g.kt128 * kSfTile;
-        const uint8_t* asf = g.a_sf + (int64_t)(m0 >> 7) * g.kt128 * kSfTile;
         int n_load = 0;
         for (int i = 0; i < nk; i++) {
             const int s = i % S;
@@ -155,9 +153,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) {
                 mbar_arrive_expect_tx(&full[s], RT * kRowB + NT * kRowB + 2 * sfb);
                 tma_load_2d(sW + s * kWTile + row0 * kRowB, &tmap_b, &full[s], i * kRowB, n0);
-                tma_load_2d(sX + s * NT * kRowB, &tmap_a, &full[s], i * kRowB, m0);
+                tma_load_2d(sX + s * NT * kRowB, &tmap_a, &full[s], i * kRowB, 0);
                 bulk_load(sSw + s * 2 * kSfTile, bsf + (int64_t)2 * i * kSfTile, sfb, &full[s]);
-                bulk_load(sSx + s * 2 * kSfTile, asf + (int64_t)2 * i * kSfTile, sfb, &full[s]);
+                bulk_load(sSx + s * 2 * kSfTile, g.a_sf + (int64_t)2 * i * kSfTile, sfb, &full[s]);
             }
             __syncwarp();
             n_load++;
@@ -217,17 +215,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mbar_wait_warp(accfull, 0, abort_flag, g.st)) {
             tc_fence_after();
             const bool in = r >= row0 && r < row0 + RT && n < g.N;
-            const int tokens = min(NT, g.M - m0);
             const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16);
-            for (int c = 0; c < tokens; c += 16) {
-                uint32_t d[16];
-                tmem_ld16(taddr + (uint32_t)c, d);
-                tmem_ld_wait();
+            const auto walk = [&](auto* out) {
+                out += n;
+                for (int c = 0; c < g.M; c += 16) {
+                    uint32_t d[16];
+                    tmem_ld16(taddr + (uint32_t)c, d);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; j++)
-                    if (in && c + j < tokens)
-                        store_out(g.out, g.dtype, (int64_t)(m0 + c + j) * g.ld + n, __uint_as_float(d[j]));
-            }
+                    for (int j = 0; j < 16; j++)
+                        if (in && c + j < g.M) {
+                            put(out, __uint_as_float(d[j]));
+                            out += g.ld;
+                        }
+                }
+            };
+            if (g.dtype == CSA_DT_BF16) walk(reinterpret_cast<__nv_bfloat16*>(g.out));
+            else if (g.dtype == CSA_DT_F16) walk(reinterpret_cast<__half*>(g.out));
+            else walk(reinterpret_cast<float*>(g.out));
             tc_fence_before();
         }
         __threadfence();   // visible before the next kernel's reads ahead of its own wait
@@ -574,7 +579,7 @@ cudaError_t run(const uint8_t* a, const uint8_t* b, const GemmArgs& g, int RT, c
     cudaError_t e = allow_smem(mxfp4_gemm_kernel<NT>, sm, done);
     if (e != cudaSuccess) return e;
     LaunchScope scope(kKMxMatmul, stream);
-    return launch_pdl(mxfp4_gemm_kernel<NT>, dim3((g.N + RT - 1) / RT, (g.M + NT - 1) / NT),
+    return launch_pdl(mxfp4_gemm_kernel<NT>, dim3((g.N + RT - 1) / RT),
                       dim3(kThreads), sm, stream, mb, ma, g, RT);
 }
 
@@ -592,7 +597,8 @@ cudaError_t run_wide(const uint8_t* a, const uint8_t* b, const GemmArgs& g, int 
         !make_map(&ma, a, (uint64_t)g.M, (uint64_t)g.K / 2, 128u))
         return cudaErrorInvalidValue;
     // The TMA unit stores where it can: rows 16-byte aligned and whole 16-byte pieces (it writes a
-    // row's last piece whole, past the row's end), byte columns within an int32.
+    // row's last piece whole, past the row's end), byte columns within an int32.  512 x 8192 x
+    // 2048: 7.9 us, with the threads' own stores 8.4; 128 x 8192 x 2048: 6.2 and 5.9.
     const uint64_t pitch = (uint64_t)g.ld * sizeof(T);
     const int tma_out = (reinterpret_cast<uintptr_t>(g.out) | pitch | (uint64_t)g.N * sizeof(T)) % 16 == 0 &&
                         (uint64_t)g.N * sizeof(T) < (1ull << 31) && pitch < (1ull << 40);
@@ -625,12 +631,15 @@ cudaError_t launch_mxfp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uin
                                 int64_t ld, int32_t* st, cudaStream_t stream) {
     const GemmArgs g{a_sf, b_sf, out, ld, st, M, N, K, dtype, (K + 127) / 128};
     const int sms = sm_count();
-    if (M > 64) {
+    // Up to 96 tokens lie on the columns: 8192 x 2048 takes 5.3 us for 32 tokens (7.1 on the lanes),
+    // 5.9 against 6.4 for 65, 6.0 against 6.0 (16384 x 2048: 6.0, 6.7) for 96; 128 tokens would take
+    // 6.3 against 6.2.
+    if (M > 96) {
         // The feature tile that takes the least time: rounds of tiles over the SMs, each a fixed part
         // and a part per stage of K (in 10 ns, from 8192 x 8192 at K = 512 and 4096: 256 columns
         // 1.6 + 0.41 per stage, 128 0.7 + 0.28, 64 0.45 + 0.27; the narrow tiles are bound by the
-        // stage's issue, not its bytes).  512 x 8192 x 2048: 10.3 us at 256, 10.8 at 128, 14.0 at
-        // 64; 197 x 4104 x 1504: 10.9, 6.8 and 5.9.
+        // stage's issue, not its bytes).  512 x 8192 x 2048: 7.8 us at 256, 9.1 at 128, 13.5 at 64;
+        // 197 x 4104 x 1504: 9.6, 7.3 and 6.4.
         const int64_t mt = (M + 127) / 128, nk = (K + kStageK - 1) / kStageK;
         auto cost = [&](int ct, int64_t fixed, int64_t per_stage) {
             return (mt * ((N + ct - 1) / ct) + sms - 1) / sms * (fixed + per_stage * nk);
@@ -640,12 +649,14 @@ cudaError_t launch_mxfp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uin
         if (c128 <= c64) return run_wide_type<128>(a, b, g, sms, stream);
         return run_wide_type<64>(a, b, g, sms, stream);
     }
-    // weight rows a CTA takes: 128, or fewer while the tiles leave SMs without one
+    // weight rows a CTA takes: 128, or fewer while the tiles leave SMs without one (8 x 8192 x 2048:
+    // 5.3 us at 64, 5.5 at 128, and 9.8 at 32 in two rounds; 8 x 16384 x 2048: 5.5 at 128, 10.0 at 64)
     int RT = 128;
     while (RT > 32 && (N + RT / 2 - 1) / (RT / 2) <= sms) RT /= 2;
     if (M <= 16) return run<16>(a, b, g, RT, stream);
     if (M <= 32) return run<32>(a, b, g, RT, stream);
-    return run<64>(a, b, g, RT, stream);
+    if (M <= 64) return run<64>(a, b, g, RT, stream);
+    return run<96>(a, b, g, RT, stream);
 }
 
 }  // namespace csa

@@ -192,6 +192,27 @@ def test_matmul_rows_do_not_depend_on_the_batch():
         assert torch.equal(part.view(torch.int32), full[:, lo:lo + n].contiguous().view(torch.int32))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 31, 32, 33, 47, 49, 63, 64, 65, 79, 95, 96, 97])
+def test_matmul_every_token_tile_width(M, dt):
+    # both sides of each width of the token tile: exact sums (K = 1504 keeps them below 2^20 / 16),
+    # nothing written past the N columns or the M rows, and wide scales with the bits of a larger
+    # batch
+    rng = np.random.default_rng(M)
+    N, K = 215, 1504
+    a, b = _operands(rng, M, N, K, 126, 127)
+    out = torch.full((M + 2, N + 3), 3.0, dtype=DT[dt], device=DEV)
+    st = _status()
+    L.csa_mxfp4_matmul(_gpu(a[0]), _gpu(io.tile_scales(a[1])), _gpu(b[0]), _gpu(io.tile_scales(b[1])),
+                       out[:M, :N], dev_status=st)
+    _sync(st)
+    assert torch.equal(out[:M, :N].cpu(), torch.from_numpy(a[2] @ b[2].T).to(DT[dt]))
+    assert bool((out[M:] == 3.0).all()) and bool((out[:, N:] == 3.0).all())
+    a, b = _operands(rng, 130, N, K, 115, 139)
+    full = _matmul(a, b, dt)
+    assert torch.equal(_matmul([x[5:5 + M] for x in a], b, dt), full[5:5 + M])
+
+
 def test_matmul_nan_scales_reach_their_results_only():
     rng = np.random.default_rng(6)
     M, N, K = 20, 140, 160
