@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_kernel(
         // what is left from here, at most a task's worth; past the end nothing is
         const int rows_left = (int)max(min(rows - row, (int64_t)64), (int64_t)0);
         const int pad_rows_left = (int)max(min(tk.rows - row, (int64_t)64), (int64_t)0);
-        const uint32_t units_left = unit < units ? units - unit : 0u, pad_units_left = unit < tk.units ? tk.units - unit : 0u;
+        const uint32_t units_left = unit < units ? units - unit : 0u;
+        const uint32_t pad_units_left = unit < tk.units ? tk.units - unit : 0u;
         const T* src = x + row * ld + unit * 8;
         uint32_t* dst = codes + row * units + unit;
         uint8_t* sfp = sf + sm.at(row, unit >> 2);

@@ -195,9 +195,10 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const QkArgs 
 //   division, the product, the definition's rounding of the scale to fp32: 11 u.
 // The bracket's own roundings add 2 u.  Counted whole against |v1| + |v2|, the bound of e4m3, whose
 // codes are dense near zero, sent 1 pass in 15 to fp64, where this sends 1 in 38 (8192 tokens of
-// 64 x 128: 72 -> 68 us; MXFP4 sends 1 in 200 either way).  With rows' sums of squares below 2^100, weights below 2^40 and results within 2^-60 .. 2^100 nothing
-// overflows, and an underflowed product is below 2^-34 of a quotient's unit, far from every
-// border but zero's, whose sign it keeps.
+// 64 x 128: 72 -> 68 us; MXFP4 sends 1 in 200 either way).  With rows' sums of squares below
+// 2^100, weights below 2^40 and results within 2^-60 .. 2^100 nothing overflows, and an
+// underflowed product is below 2^-34 of a quotient's unit, far from every border but zero's,
+// whose sign it keeps.
 constexpr float kU24 = 5.9604645e-08f;
 constexpr float kAbsMargin = 5.f * kU24, kRelMargin = 15.f * kU24, kTopMargin = 24.f * kU24;
 constexpr float kTiny = 8.6736174e-19f, kHuge = 1.2676506e+30f;   // 2^-60, 2^100

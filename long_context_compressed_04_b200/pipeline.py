@@ -12,8 +12,9 @@ import torch
 
 from . import (CSA_IDX_FP8, CSA_KV_BF16, CSA_SF_TILED, csa_compress, csa_entry_row_bytes,
                csa_indexer_queries, csa_indexer_workspace_size, csa_mxfp4_matmul,
-               csa_mxfp4_quantize, csa_mxfp4_sf_bytes, dense_hca_attn, dense_hca_workspace_size, hca_compress, lightning_indexer_topk,
-               lightning_indexer_topk_mxfp4, sparse_mqa_attn)
+               csa_mxfp4_quantize, csa_mxfp4_sf_bytes, dense_hca_attn, dense_hca_workspace_size,
+               hca_compress, lightning_indexer_topk, lightning_indexer_topk_mxfp4,
+               sparse_mqa_attn)
 from .synth import Workload
 
 
