@@ -328,10 +328,16 @@ struct RotTable {
     float2 f32[64];
 };
 
-// Weights of a call without any (read like the others: no branch per row).
+// Weights of a call without any (read like the others: no branch per row, 16 bytes at a time, which
+// a bare array of floats would not be aligned for).
 #define CSA_ONES_8 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f
 #define CSA_ONES_32 CSA_ONES_8, CSA_ONES_8, CSA_ONES_8, CSA_ONES_8
-__device__ const float kOnes[128] = {CSA_ONES_32, CSA_ONES_32, CSA_ONES_32, CSA_ONES_32};
+constexpr int kMaxIndexerDim = 128;
+struct alignas(sizeof(float4)) UnitWeights {
+    float v[kMaxIndexerDim];
+};
+static_assert(alignof(UnitWeights) >= alignof(float4), "read through float4");
+__device__ const UnitWeights kOnes = {{CSA_ONES_32, CSA_ONES_32, CSA_ONES_32, CSA_ONES_32}};
 
 // What a lane needs of a position: its weights, its chunks' pairs in the table, whether a weight
 // is past what the fast path's bound holds for.
@@ -516,8 +522,9 @@ __device__ __forceinline__ void fill_table(RotTable& t, const RopeTable& rt, dou
 
 template <int LPR, RotMode RM>
 __device__ __forceinline__ LaneParams<RM> lane_params(const float* weight, const RotTable& table, int l, int rope) {
+    static_assert(8 * kC * LPR <= kMaxIndexerDim, "a row's channels each have a unit weight");
     LaneParams<RM> p;
-    p.weight = (weight ? weight : kOnes) + 8 * l;
+    p.weight = (weight ? weight : kOnes.v) + 8 * l;
     p.table = &table;
     p.past = false;
 #pragma unroll

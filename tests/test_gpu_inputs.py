@@ -717,3 +717,29 @@ def test_compiled_and_python_marshalling_agree(monkeypatch):
         assert fast[1] == slow[1]
         for a, b in zip(fast[0], slow[0]):
             assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("fmt", [L.CSA_IDX_FP8, L.CSA_IDX_MXFP4])
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_no_weight_is_a_weight_of_ones(D, dt, fmt):
+    # the unit weight that a call without one reads, on every kernel that reads it
+    g = torch.Generator(device=DEV).manual_seed(D)
+    x = torch.randn((19, 6, D), generator=g, device=DEV).to(DT[dt])
+    pos = torch.randint(0, 1 << 20, (19,), generator=g, device=DEV, dtype=torch.int32)
+    item = torch.arange(19, dtype=torch.int32, device=DEV)
+    seq_len, off = torch.tensor([80], device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV)
+    for rope in (64, 32):
+        got = []
+        for w in (None, torch.ones(D, device=DEV)):
+            qc, qs = _store(fmt, (19, 6), D)
+            kc, ks = _store(fmt, (20,), D)
+            L.csa_indexer_queries(x, pos, qc, qs, fmt=fmt, weight=w, rope_dims=rope)
+            L.csa_indexer_append(x[:, 2], seq_len, off, torch.zeros_like(item), item, kc, ks, B=1, fmt=fmt, weight=w,
+                                 rope_dims=rope)
+            got.append((qc, qs, kc, ks))
+        torch.cuda.synchronize()
+        for a, b in zip(*got):
+            assert torch.equal(a, b)
+        y = io.norm_rope(f64(x), pos.cpu().numpy(), rope=rope)
+        _same(got[0][0], got[0][1], _quant_ref(y, fmt))
