@@ -8,6 +8,7 @@ been built (``python long_context_compressed_04_b200/build.py``).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -666,7 +667,7 @@ def csa_indexer_append(k, seq_len, ent_off, item_seq, item_ent, codes, scale, *,
                        layout=None, dev_status=None, stream=None):
     """Indexer keys k [n, D] of the listed entries normed, rotated at their block ends,
     quantised and written to their rows of the key store (codes, scale), through the layout's
-    block table or ent_off."""
+    block table or ent_off.  A block table that is a slice of columns is copied first."""
     bt, ring = None, 0
     if layout is not None:
         bt, ring = getattr(layout, "_block_table", None), layout.kv_ring
@@ -678,6 +679,14 @@ def csa_indexer_append(k, seq_len, ent_off, item_seq, item_ent, codes, scale, *,
             return
         if status is not None:
             _check(status)
+    if bt is not None and bt.dim() == 2:
+        # The kernel takes the table's stride for its width.  Rows with a gap between them (a
+        # slice of columns) are copied: an entry past the slice would find the next row's
+        # blocks, or, behind the last row, what is no table at all.
+        if B > 1 and bt.stride(0) != bt.shape[1]:
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                bt = bt[:B].contiguous()
+        layout = CacheLayout(bt.data_ptr(), bt.shape[1], ring)
     dev, dtype = k.get_device(), _DTYPES.get(k.dtype)
     if k.dim() != 2:
         _need_2d(k, "k")

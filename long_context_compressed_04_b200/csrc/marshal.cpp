@@ -311,11 +311,13 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     csa_cache_layout_t layout = {nullptr, 0, x.integer(16)};
     if (!x.none(15)) {
         const at::Tensor* bt = x.tensor(15);
+        // the kernel takes the stride for a row's width: rows with a gap go to the Python side
         x.need(bt && bt->scalar_type() == at::kInt && bt->dim() == 2 && bt->size(0) >= B &&
-               (bt->stride(1) == 1 || bt->size(1) <= 1) && bt->get_device() == k.dev);
+               (bt->stride(1) == 1 || bt->size(1) <= 1) && (bt->stride(0) == bt->size(1) || B == 1) &&
+               bt->get_device() == k.dev);
         if (!x.ok) Py_RETURN_NONE;
         layout.block_table = static_cast<const int32_t*>(bt->data_ptr());
-        layout.bt_stride = bt->stride(0);
+        layout.bt_stride = bt->size(1);
     }
     x.need(k.cols <= INT32_MAX);
     int32_t* st = x.status(17, k.dev);

@@ -743,3 +743,45 @@ def test_no_weight_is_a_weight_of_ones(D, dt, fmt):
             assert torch.equal(a, b)
         y = io.norm_rope(f64(x), pos.cpu().numpy(), rope=rope)
         _same(got[0][0], got[0][1], _quant_ref(y, fmt))
+
+
+@pytest.mark.parametrize("compiled", [True, False])
+@pytest.mark.parametrize("fmt", [L.CSA_IDX_FP8, L.CSA_IDX_MXFP4])
+def test_append_through_a_slice_of_a_block_table(fmt, compiled, monkeypatch):
+    # a slice of columns: the same rows as through a table of its own; entries past the slice (whose
+    # blocks a wider table has) are flagged and written nowhere, whatever the sequences' lengths
+    if not compiled:
+        monkeypatch.setattr(L, "_marshal", None)
+    g = torch.Generator(device=DEV).manual_seed(31)
+    big = torch.randperm(24, generator=g, device=DEV).to(torch.int32).view(3, 8)
+    k = torch.randn((7, 128), generator=g, device=DEV)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    seq, ent = i32(0, 1, 2, 2, 1, 0, 2), i32(0, 40, 95, 96, 100, 255, 200)
+    seq_len = torch.full((3,), 4 * 256, dtype=torch.int64, device=DEV)
+    side = torch.cuda.Stream()
+    for view in (big[:, 2:5], big[:, 5:], big[:, :3]):
+        want_c, want_s = _store(fmt, (24 * 32,), 128)
+        st = _status()
+        L.csa_indexer_append(k[:3], seq_len, None, seq[:3], ent[:3], want_c, want_s, B=3, fmt=fmt,
+                             layout=L.cache_layout(view.contiguous()), dev_status=st)
+        _sync(st)
+        for stream in (None, side):
+            codes, scale = _store(fmt, (24 * 32,), 128)
+            torch.cuda.synchronize()
+            L.csa_indexer_append(k, seq_len, None, seq, ent, codes, scale, B=3, fmt=fmt,
+                                 layout=L.cache_layout(view), dev_status=st, stream=stream)
+            _sync(st, L.CSA_DEV_OOB)
+            st.zero_()
+            assert torch.equal(codes, want_c) and torch.equal(scale, want_s)
+    # one sequence: its row alone, in a table with a gap behind it
+    codes, scale = _store(fmt, (24 * 32,), 128)
+    st = _status()
+    L.csa_indexer_append(k[:2], seq_len[:1], None, i32(0, 0), i32(64, 96), codes, scale, B=1, fmt=fmt,
+                         layout=L.cache_layout(big[2:, 5:]), dev_status=st)
+    _sync(st, L.CSA_DEV_OOB)
+    row = int(big[2, 7]) * 32
+    y = io.norm_rope(f64(k)[:1, None], np.array([65 * 4 - 1]))[:, 0]
+    _same(codes[row:row + 1], scale[row:row + 1], _quant_ref(y, fmt))
+    codes[row], scale[row] = 0x11, scale[(row + 1) % 768]
+    blank = _store(fmt, (24 * 32,), 128)
+    assert torch.equal(codes, blank[0]) and torch.equal(scale, blank[1])

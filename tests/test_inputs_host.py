@@ -211,3 +211,28 @@ def test_binding_refuses_tensors_it_would_read_past():
         L.csa_indexer_append(k, i64, i64, i32, i32, u8(9, 128), torch.zeros(9), B=3)
     with pytest.raises(L.CSAError, match="scale must be"):
         L.csa_indexer_append(k, i64, i64, i32, i32, u8(9, 128), torch.zeros(8), B=2)
+
+
+def test_append_reads_no_block_past_a_slice_of_the_table(monkeypatch):
+    # what the library is handed: the bound it tests an entry's block against (the stride) is the
+    # width of the table that the caller gave, and its rows are those of that table
+    seen = []
+
+    def call(*a):
+        lay = a[20]._obj
+        assert lay.bt_stride == table.shape[1]
+        rows = ctypes.cast(lay.block_table, ctypes.POINTER(ctypes.c_int32))
+        seen.extend(rows[i] for i in range(a[8] * lay.bt_stride))
+        return 0
+
+    monkeypatch.setattr(L, "_marshal", None)
+    monkeypatch.setattr(L, "_idx_append", call)
+    monkeypatch.setattr(L, "_is_current", lambda dev: True)
+    monkeypatch.setattr(L, "_stream_on", lambda stream, dev: None)
+    big = torch.arange(40, dtype=torch.int32).view(4, 10)
+    for table, B in ((big, 4), (big[:, 2:], 4), (big[:, 3:6], 3), (big[2:, :4], 2), (big[3:, 7:], 1), (big[1:], 1)):
+        k, i32 = torch.zeros((5, 128)), torch.zeros(5, dtype=torch.int32)
+        L.csa_indexer_append(k, torch.zeros(B, dtype=torch.int64), None, i32, i32, torch.zeros((9, 128), dtype=torch.uint8),
+                             torch.zeros(9), B=B, layout=L.cache_layout(table))
+        assert seen == table[:B].flatten().tolist()
+        seen.clear()
