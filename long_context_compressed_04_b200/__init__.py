@@ -11,6 +11,8 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import sys
+import warnings
 
 import torch
 
@@ -322,7 +324,8 @@ def dense_hca_attn(q, entries, seq_len, ent_off, kv, kv_off, kv_pos0, q_seq, q_p
 # read past its end; sizes and alignments are checked by the library.  Decode steps issue many
 # small launches, and the host time per call is what bounds them: the tests and the
 # conversion of the arguments are compiled (csrc/marshal.cpp).  Where a test fails, or that
-# module was not built, the call below does the same in Python, finds the reason and raises.
+# module was not built for this torch, the call below does the same in Python, finds the reason
+# and raises.
 _DTYPES = {torch.bfloat16: CSA_DT_BF16, torch.float16: CSA_DT_F16, torch.float32: CSA_DT_F32}
 _U8, _I32T, _I64T, _F32T = torch.uint8, torch.int32, torch.int64, torch.float32
 # The current stream's handle without a Stream object (3 us less per call) and the current
@@ -336,12 +339,24 @@ _qk_norm_rope, _idx_queries, _idx_append = (_lib.csa_qk_norm_rope, _lib.csa_inde
                                             _lib.csa_indexer_append)
 
 
-try:
-    from . import _csa_marshal as _marshal
-    _marshal.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+def _load_marshal():
+    """The compiled marshalling, or None where it was not built, or was built against another
+    torch or Python, whose tensors it would read at the wrong places."""
+    try:
+        from . import _csa_marshal as m
+    except ImportError:
+        return None
+    built = getattr(m, "torch_version", None), getattr(m, "python_tag", None)
+    if built != (str(torch.__version__), sys.implementation.cache_tag):
+        warnings.warn(f"_csa_marshal.so was built for torch {built[0]} ({built[1]}) and is not used: "
+                      "build the package again")
+        return None
+    m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         _mx_quantize, _mx_dequantize, _mx_matmul, _qk_norm_rope, _idx_queries, _idx_append)))
-except ImportError:
-    _marshal = None
+    return m
+
+
+_marshal = _load_marshal()
 
 
 def _handle(stream):

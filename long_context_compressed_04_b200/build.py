@@ -53,22 +53,30 @@ def build_marshal(force: bool = False) -> str:
 
     import torch
     src = os.path.join(CSRC, "marshal.cpp")
-    if not (force or _stale(MARSHAL, [src, os.path.join(ROOT, "include", "csa.h")])):
-        return MARSHAL
     troot = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = MARSHAL + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-shared", "-fPIC",
            "-std=c++17", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DCSA_TORCH="{torch.__version__}"', f'-DCSA_PYTHON="{sys.implementation.cache_tag}"',
            "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(troot, "include"),
            "-isystem", os.path.join(troot, "include", "torch", "csrc", "api", "include"),
-           "-isystem", os.path.join(cuda, "include"), src, "-o", tmp,
+           "-isystem", os.path.join(cuda, "include"), src,
            "-L" + os.path.join(troot, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    # torch's headers are not among the files looked at: the command, which names their version,
+    # is kept beside the objects, and another one builds again
+    stamp = os.path.join(OBJ_DIR, "marshal.cmd")
+    same = os.path.exists(stamp) and open(stamp).read() == "\n".join(cmd)
+    if same and not force and not _stale(MARSHAL, [src, os.path.join(ROOT, "include", "csa.h")]):
+        return MARSHAL
+    r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("build of _csa_marshal.so failed")
     os.replace(tmp, MARSHAL)
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write("\n".join(cmd))
     return MARSHAL
 
 

@@ -376,4 +376,14 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_csa_marshal", nullptr, -1, method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__csa_marshal(void) { return PyModule_Create(&module); }
+// CSA_TORCH, CSA_PYTHON: the versions compiled against, whose tensors' layout is compiled in.  The
+// package takes the module under these alone.
+PyMODINIT_FUNC PyInit__csa_marshal(void) {
+    PyObject* m = PyModule_Create(&module);
+    if (m && (PyModule_AddStringConstant(m, "torch_version", CSA_TORCH) ||
+              PyModule_AddStringConstant(m, "python_tag", CSA_PYTHON))) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -1,6 +1,9 @@
 """Host side of the operators that make the indexer's inputs (CPU only): the 64-bit forms
 against library casts, the scale sizes, and every refusal of bad arguments before a launch."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import ml_dtypes
 import numpy as np
@@ -9,6 +12,7 @@ import torch
 
 import _inputs_orc as io
 import long_context_compressed_04_b200 as L
+from long_context_compressed_04_b200 import build
 
 P = ctypes.c_void_p
 F = P(4096)          # never dereferenced: validation fails before any launch
@@ -236,3 +240,39 @@ def test_append_reads_no_block_past_a_slice_of_the_table(monkeypatch):
                              torch.zeros(9), B=B, layout=L.cache_layout(table))
         assert seen == table[:B].flatten().tolist()
         seen.clear()
+
+
+def test_marshalling_built_for_another_torch_is_not_used():
+    # its accessors hold another torch's tensor layout: the package goes on without it
+    code = ("import torch; torch.__version__ = '0.0.1'; import long_context_compressed_04_b200 as L; "
+            "assert L._marshal is None")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr
+    assert L._marshal is not None and L._marshal.torch_version == torch.__version__
+
+
+@pytest.fixture
+def marshal_build(monkeypatch, tmp_path):
+    """build.build_marshal in a directory of its own, its compiler runs counted, not made."""
+    runs = []
+
+    def run(cmd, **kw):
+        runs.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build, "MARSHAL", str(tmp_path / "_csa_marshal.so"))
+    monkeypatch.setattr(build, "OBJ_DIR", str(tmp_path))
+    monkeypatch.setattr(build.subprocess, "run", run)
+    return runs
+
+
+def test_marshalling_is_built_again_for_another_torch(marshal_build, monkeypatch):
+    build.build_marshal()
+    build.build_marshal()
+    assert len(marshal_build) == 1
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    build.build_marshal()
+    build.build_marshal()
+    assert len(marshal_build) == 2
