@@ -4,7 +4,7 @@ Each .cu file under csrc/ compiles to an object in parallel; the objects link in
 long_context_compressed_04_b200/libcsa.so with the CUDA runtime linked statically, so the
 library needs no CUDA shared library besides the driver at run time.  csrc/marshal.cpp, the
 Python binding's compiled argument marshalling, builds beside it with the host compiler
-against the installed torch (_csa_marshal.so).
+against the installed torch (_csa_marshal.so); where that fails, the binding does without.
 """
 from __future__ import annotations
 
@@ -112,7 +112,14 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link of libcsa.so failed")
         os.replace(tmp, OUT)
-    marshal.result()
+    try:
+        marshal.result()
+    except Exception as e:      # noqa: BLE001  (no torch, no Python headers, no host compiler)
+        # the library stands without it and the binding does the same in Python, more slowly; one of
+        # an older source must not stay
+        if os.path.exists(MARSHAL):
+            os.remove(MARSHAL)
+        sys.stderr.write(f"_csa_marshal.so was not built ({type(e).__name__}: {e}): the binding goes on without it\n")
     return OUT
 
 

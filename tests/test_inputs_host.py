@@ -276,3 +276,27 @@ def test_marshalling_is_built_again_for_another_torch(marshal_build, monkeypatch
     build.build_marshal()
     build.build_marshal()
     assert len(marshal_build) == 2
+
+
+@pytest.mark.parametrize("fails", ["compiler", "compile", "headers"])
+def test_library_builds_where_the_marshalling_cannot(marshal_build, monkeypatch, capfd, fails):
+    # no host compiler, one that refuses the source, a torch without its paths: the library is built
+    # all the same, and no marshalling of an older source is left behind
+    open(build.MARSHAL, "w").close()
+    run = build.subprocess.run
+
+    def failing(cmd, **kw):
+        if cmd[0].endswith("g++"):
+            if fails == "compiler":
+                raise FileNotFoundError("g++")
+            if fails == "compile":
+                return subprocess.CompletedProcess(cmd, 1, "", "no Python.h")
+        return run(cmd, **kw)
+
+    monkeypatch.delenv("CXX", raising=False)
+    monkeypatch.setattr(build.subprocess, "run", failing)
+    monkeypatch.setattr(build, "OUT", os.path.join(build.OBJ_DIR, "libcsa.so"))
+    if fails == "headers":
+        monkeypatch.delattr(torch, "_C")
+    assert build.build(force=True) == build.OUT and os.path.exists(build.OUT)
+    assert not os.path.exists(build.MARSHAL) and "without it" in capfd.readouterr().err
