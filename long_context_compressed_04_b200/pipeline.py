@@ -122,7 +122,9 @@ def step(wl: Workload, buf: Buffers, item_seq, item_ent, stream=None):
 class QueryProjection:
     """The indexer's query heads from hidden states: an MXFP4 projection, then the heads'
     norm, rotation and quantisation (csa_mxfp4_quantize, csa_mxfp4_matmul,
-    csa_indexer_queries).  The weight is quantised once; the buffers of up to ``max_q``
+    csa_indexer_queries).  The weight is quantised once, here, and held before the constructor
+    returns, so that calls may use any stream (a block of it that is not finite sets
+    CSA_DEV_NAN in ``dev_status``, as rows of the calls do); the buffers of up to ``max_q``
     query tokens are allocated here, so calls allocate nothing and can be captured.  Calls
     share them: order calls of one projection on one stream."""
 
@@ -137,7 +139,8 @@ class QueryProjection:
         self.H_I, self.d_I, self.K, self.fmt, self.max_q = H_I, d_I, K, fmt, max_q
         self.head_weight, self.theta, self.eps = head_weight, theta, eps
         self.w, self.w_sf = u8(N, K // 2), u8(csa_mxfp4_sf_bytes(N, K, CSA_SF_TILED))
-        csa_mxfp4_quantize(weight, self.w, self.w_sf, sf_layout=CSA_SF_TILED)
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
+        csa_mxfp4_quantize(weight, self.w, self.w_sf, sf_layout=CSA_SF_TILED, dev_status=self.dev_status)
         self.x, self.x_sf = u8(max_q, K // 2), u8(csa_mxfp4_sf_bytes(max_q, K, CSA_SF_TILED))
         self.heads = torch.empty((max_q, H_I, d_I), dtype=torch.bfloat16, device=dev)
         if fmt == CSA_IDX_FP8:
@@ -145,7 +148,9 @@ class QueryProjection:
             self.scale = torch.empty((max_q, H_I), dtype=torch.float32, device=dev)
         else:
             self.codes, self.scale = u8(max_q, H_I, d_I // 2), u8(max_q, H_I, d_I // 32)
-        self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
+        # no call waits for this stream; inside a capture the graph's order has to do
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
 
     def __call__(self, x: torch.Tensor, q_pos: torch.Tensor, stream=None):
         """x [Q, K] (bf16, fp16 or fp32), q_pos int32 [Q]: the query heads' codes and scales,

@@ -262,3 +262,23 @@ def test_normed_queries_go_straight_into_the_attention():
     for r in range(20):
         assert torch.equal(got[r], want[r % 5]), r
     assert torch.equal(out, want[19 % 5])
+
+
+def test_projection_on_another_stream_than_it_was_built_on():
+    # the building stream is busy; the first call goes to another one.  A weight with a NaN is
+    # reported where the calls report
+    g = torch.Generator(device=DEV).manual_seed(31)
+    proj_w = (torch.randn((HI * DI, K), generator=g, device=DEV) / 16).to(torch.bfloat16)
+    x, pos = _hidden(g, 4), torch.arange(4, dtype=torch.int32, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    proj = pipeline.QueryProjection(proj_w, HI, DI, max_q=4)
+    qI, qs = proj(x, pos, stream=side)
+    side.synchronize()
+    ref = _heads_ref(x, proj_w, pos, torch.ones(DI), L.CSA_IDX_FP8)
+    assert np.array_equal(qI.cpu().numpy(), ref[0])
+    _same_scales(qs, ref[1])
+    assert int(proj.dev_status.item()) == 0
+    proj_w[77, 5] = float("nan")
+    assert int(pipeline.QueryProjection(proj_w, HI, DI, max_q=4).dev_status.item()) == L.CSA_DEV_NAN

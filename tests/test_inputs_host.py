@@ -12,7 +12,7 @@ import torch
 
 import _inputs_orc as io
 import long_context_compressed_04_b200 as L
-from long_context_compressed_04_b200 import build
+from long_context_compressed_04_b200 import build, pipeline
 
 P = ctypes.c_void_p
 F = P(4096)          # never dereferenced: validation fails before any launch
@@ -300,3 +300,20 @@ def test_library_builds_where_the_marshalling_cannot(marshal_build, monkeypatch,
         monkeypatch.delattr(torch, "_C")
     assert build.build(force=True) == build.OUT and os.path.exists(build.OUT)
     assert not os.path.exists(build.MARSHAL) and "without it" in capfd.readouterr().err
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_projection_is_complete_when_built(monkeypatch, capturing):
+    # the weight's quantisation reports to the projection's status and is waited for (not inside a
+    # capture), so that a first call on another stream reads all of it
+    events = []
+
+    class Stream:
+        def synchronize(self):
+            events.append("wait")
+
+    monkeypatch.setattr(pipeline, "csa_mxfp4_quantize", lambda x, c, s, **kw: events.append(kw["dev_status"]))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    p = pipeline.QueryProjection(torch.zeros((256, 64)), 2, 128, max_q=3)
+    assert events[0] is p.dev_status and events[1:] == ([] if capturing else ["wait"])
