@@ -15,10 +15,12 @@ attends (``sparse_mqa_attn``), every call with the same cache layout.  Indexer k
 ready-made with the token, or as bf16 / fp32 rows that ``append_keys`` norms, rotates and
 quantises on the way into their blocks (``csa_indexer_append``); the key store holds FP8 or
 MXFP4 rows.  This module keeps the host-side bookkeeping (block allocation, the item lists of
-completed entries); every copy, compression, score, selection and attention runs in libcsa.
+completed entries, which entries have their key yet: ``select`` refuses queries that see one
+without); every copy, compression, score, selection and attention runs in libcsa.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import List, Optional
 
 import torch
@@ -46,6 +48,16 @@ class BlockAllocator:
 
     def release(self, blocks):
         self.free.extend(int(x) for x in blocks)
+
+
+class Items(tuple):
+    """(item_seq, item_ent) of entries on the device, with the same as host lists."""
+
+    def __new__(cls, seqs: List[int], ents: List[int], device):
+        self = super().__new__(cls, (torch.tensor(seqs, dtype=torch.int32, device=device),
+                                     torch.tensor(ents, dtype=torch.int32, device=device)))
+        self.host = (seqs, ents)
+        return self
 
 
 class HybridCache:
@@ -77,6 +89,9 @@ class HybridCache:
         self.bt_host = torch.full((B, max_blocks), -1, dtype=torch.int32)
         self.seq_len = torch.zeros(B, dtype=torch.int64, device=dev)
         self.len_host = [0] * B
+        # a byte per entry of a sequence: its key is in the store; and the complete entries without
+        self._keyed = [bytearray(max_blocks * BLOCK_ENTRIES) for _ in range(B)]
+        self._unkeyed = [0] * B
         self.alloc = BlockAllocator(n_blocks)
         self.layout = cache_layout(self.block_table, kv_ring=ring)
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
@@ -100,8 +115,59 @@ class HybridCache:
         self.alloc.release(blocks)
         self.bt_host[b] = -1
         self.len_host[b] = 0
+        self._set_keyed(b, 0, False)
         self._push_table()
         self.seq_len[b] = 0
+
+    # ---- which entries have their indexer key -----------------------------------------
+    def _set_keyed(self, b: int, n: int, keyed: bool):
+        """Sequence b anew, with n entries that all have their keys or all lack them."""
+        size = len(self._keyed[b])
+        self._keyed[b] = bytearray((b"\1" * n if keyed else b"").ljust(size, b"\0"))
+        self._unkeyed[b] = 0 if keyed else n
+
+    def note_keys(self, items, stream=None):
+        """Entries items[1][j] of sequences items[0][j] have their indexer keys in the store:
+        append_keys calls it, and so does one who writes to the store otherwise (a replayed
+        graph, say).  Lists that append() returned cost nothing; others are read back from the
+        device while entries lack keys, and count as all of those during a stream capture, when
+        they cannot be."""
+        if not any(self._unkeyed):
+            return
+        if isinstance(items, Items):
+            seqs, ents = items.host
+        elif self._capturing(stream):
+            for b in range(self.B):
+                self._set_keyed(b, self.len_host[b] // M, True)
+            return
+        else:
+            seqs, ents = self._read(stream, *items)
+        for b, i in zip(seqs, ents):
+            if 0 <= b < self.B and 0 <= i < self.len_host[b] // M and not self._keyed[b][i]:
+                self._keyed[b][i] = 1
+                self._unkeyed[b] -= 1
+
+    def _on(self, stream):
+        return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+    def _capturing(self, stream):
+        with self._on(stream):
+            return self.device.type == "cuda" and torch.cuda.is_current_stream_capturing()
+
+    def _read(self, stream, *tensors):
+        with self._on(stream):
+            return [t.tolist() for t in tensors]
+
+    def _check_keys(self, q_seq, q_pos, stream):
+        """Refuses queries that see an entry without its key."""
+        if self._capturing(stream):
+            return
+        for b, p in zip(*self._read(stream, q_seq, q_pos)):
+            if 0 <= b < self.B and self._unkeyed[b]:
+                i = self._keyed[b].find(0, 0, min((p + 1) // M, self.len_host[b] // M))
+                if i >= 0:
+                    raise RuntimeError(f"entry {i} of sequence {b} has no indexer key: append_keys "
+                                       "brings it (note_keys where something else wrote it)")
 
     # ---- loading a prefix (set-up) -----------------------------------------------
     def load_prefix(self, b: int, kv_tail, gate_tail, T: int, entries, kI=None, ks=None):
@@ -124,6 +190,7 @@ class HybridCache:
             self.ks[rows] = ks
         self.seq_len[b] = T
         self.len_host[b] = T
+        self._set_keyed(b, n, kI is not None)
 
     # ---- one decode step -----------------------------------------------------------
     def append(self, kv_new, gate_new, kI_new=None, ks_new=None, stream=None):
@@ -147,10 +214,12 @@ class HybridCache:
         for b in range(self.B):
             self.len_host[b] += 1
             if self.len_host[b] % M == 0:
+                i = self.len_host[b] // M - 1
                 seqs.append(b)
-                ents.append(self.len_host[b] // M - 1)
-        return (torch.tensor(seqs, dtype=torch.int32, device=self.device),
-                torch.tensor(ents, dtype=torch.int32, device=self.device))
+                ents.append(i)
+                self._keyed[b][i] = kI_new is not None
+                self._unkeyed[b] += kI_new is None
+        return Items(seqs, ents, self.device)
 
     def append_keys(self, items, k, weight=None, norm: bool = True, rope_dims: int = 64,
                     rope_theta=10000.0, eps=1e-6, stream=None):
@@ -164,6 +233,7 @@ class HybridCache:
                            fmt=self.idx_fmt, weight=weight, norm=norm, rope_dims=rope_dims,
                            rope_theta=rope_theta, eps=eps, layout=self.layout,
                            dev_status=self.dev_status, stream=stream)
+        self.note_keys(items, stream)
 
     def compress(self, items, bias, rope_theta=10000.0, eps=1e-6, stream=None):
         seq, ent = items
@@ -177,7 +247,10 @@ class HybridCache:
                workspace: Optional[torch.Tensor] = None, stream=None,
                select_bf16: bool = False):
         """Top-k of every query; qI, qs: e4m3 codes and fp32 scales, or with an MXFP4 key
-        store packed codes and scale bytes (select_bf16 as in lightning_indexer_topk_mxfp4)."""
+        store packed codes and scale bytes (select_bf16 as in lightning_indexer_topk_mxfp4).
+        Queries that see an entry whose key was never brought are refused (RuntimeError)."""
+        if any(self._unkeyed):
+            self._check_keys(q_seq, q_pos, stream)
         max_n = max(self.len_host) // M
         if workspace is None:
             workspace = torch.empty(max(csa_indexer_workspace_size(q_seq.numel(), max(max_n, 1), k), 256),
@@ -202,4 +275,4 @@ class HybridCache:
                         layout=self.layout, dev_status=self.dev_status, stream=stream)
 
 
-__all__ = ["BlockAllocator", "HybridCache", "BLOCK_TOKENS", "BLOCK_ENTRIES", "CSA_KV_BF16"]
+__all__ = ["BlockAllocator", "HybridCache", "Items", "BLOCK_TOKENS", "BLOCK_ENTRIES", "CSA_KV_BF16"]

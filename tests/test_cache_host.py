@@ -55,3 +55,88 @@ def test_layout_validation_on_the_host():
     st = lib.csa_compress(fake, fake, fake, fake, fake, fake, None, fake, fake, 1, 1, 128, 0,
                           10000.0, 1e-6, fake, None, None, None)
     assert st == 1 and b"ent_off" in lib.csa_last_error()
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The library's calls that the cache makes, named in order instead of made."""
+    seen = []
+    for name in ("csa_cache_append", "csa_indexer_append", "lightning_indexer_topk", "lightning_indexer_topk_mxfp4"):
+        monkeypatch.setattr(cache, name, lambda *a, _n=name, **kw: seen.append(_n))
+    return seen
+
+
+def _decode_cache(idx_fmt, B=2):
+    hc = cache.HybridCache(B, 128, L.CSA_KV_BF16, 128, n_blocks=8, max_blocks=4, device="cpu", idx_fmt=idx_fmt)
+    kv = torch.zeros((B, 128), dtype=torch.bfloat16)
+
+    def select(q_pos=None, seqs=None):
+        seqs = list(range(B)) if seqs is None else seqs
+        q_pos = [hc.len_host[b] - 1 for b in seqs] if q_pos is None else q_pos
+        hc.select(None, None, None, torch.tensor(seqs, dtype=torch.int32), torch.tensor(q_pos, dtype=torch.int32),
+                  None, H_I=64, k=8)
+    return hc, kv, select
+
+
+@pytest.mark.parametrize("idx_fmt", [L.CSA_IDX_FP8, L.CSA_IDX_MXFP4])
+def test_select_refuses_entries_without_their_key(calls, idx_fmt):
+    hc, kv, select = _decode_cache(idx_fmt)
+    k = torch.zeros((2, 128), dtype=torch.bfloat16)
+    for _ in range(3):
+        assert hc.append(kv, kv)[0].numel() == 0
+    select()                                       # no entry yet
+    items = hc.append(kv, kv)                      # entry 0 of both sequences
+    assert isinstance(items, tuple) and items[0].tolist() == [0, 1] and items[1].tolist() == [0, 0]
+    with pytest.raises(RuntimeError, match="entry 0 of sequence 0 has no indexer key"):
+        select()
+    select([2, 2])                                 # queries that see no entry
+    hc.append_keys((items[0][1:], items[1][1:]), k[1:])
+    select(seqs=[1])
+    with pytest.raises(RuntimeError, match="sequence 0"):
+        select()
+    hc.append_keys(items, k)                       # an entry twice counts once
+    select()
+    for _ in range(4):
+        items2 = hc.append(kv, kv)
+    hc.append_keys(items, k)                       # the wrong entries
+    with pytest.raises(RuntimeError, match="entry 1 of sequence 0"):
+        select()
+    hc.note_keys(items2)                           # brought by other means
+    select()
+    n = len(calls)
+    hc.append_keys((items2[0][:0], items2[1][:0]), k[:0])
+    assert len(calls) == n and calls.count("csa_indexer_append") == 3
+
+
+def test_select_refuses_a_prefix_and_a_reused_sequence_without_keys(calls):
+    hc, kv, select = _decode_cache(L.CSA_IDX_FP8)
+    row = L.csa_entry_row_bytes(L.CSA_KV_BF16, 128)
+    ents, kI, ks = torch.zeros((50, row), dtype=torch.uint8), torch.zeros((50, 128), dtype=torch.uint8), torch.ones(50)
+    tail = torch.zeros((128, 128), dtype=torch.bfloat16)
+    hc.load_prefix(0, tail, tail, 201, ents, kI, ks)
+    hc.load_prefix(1, tail, tail, 201, ents)
+    select(seqs=[0])
+    with pytest.raises(RuntimeError, match="entry 0 of sequence 1"):
+        select()
+    i = torch.arange(50, dtype=torch.int32)
+    bad = torch.tensor([-1, 1, 1, 7], dtype=torch.int32), torch.tensor([0, 50, -1, 0], dtype=torch.int32)
+    hc.append_keys(bad, torch.zeros((4, 128)))     # entries that are not there (flagged by the call itself)
+    hc.append_keys((torch.ones_like(i[:49]), i[:49]), torch.zeros((49, 128)))
+    select([196, 196])                             # sees 49 entries
+    with pytest.raises(RuntimeError, match="entry 49 of sequence 1"):
+        select([200, 199])
+    hc.append_keys((torch.ones_like(i[49:]), i[49:]), torch.zeros((1, 128)))
+    select()
+    # the next user of a sequence has no keys of the last one's
+    hc.release(1)
+    select()
+    hc.load_prefix(1, tail, tail, 100, ents[:25])
+    with pytest.raises(RuntimeError, match="entry 0 of sequence 1"):
+        select()
+    hc.load_prefix(1, tail, tail, 100, ents[:25], kI[:25], ks[:25])
+    select()
+    # ready-made keys with the tokens
+    for _ in range(5):
+        hc.append(kv, kv, torch.zeros((2, 128), dtype=torch.uint8), torch.ones(2))
+    select()
+    assert hc._unkeyed == [0, 0]

@@ -282,3 +282,51 @@ def test_projection_on_another_stream_than_it_was_built_on():
     assert int(proj.dev_status.item()) == 0
     proj_w[77, 5] = float("nan")
     assert int(pipeline.QueryProjection(proj_w, HI, DI, max_q=4).dev_status.item()) == L.CSA_DEV_NAN
+
+
+@pytest.mark.parametrize("fmt", [L.CSA_IDX_FP8, L.CSA_IDX_MXFP4])
+def test_select_refuses_missing_keys_on_any_stream_and_inside_a_capture(fmt):
+    # lists on the device are read on the stream they are used on; a capture reads nothing
+    g = torch.Generator(device=DEV).manual_seed(37)
+    hc = cache.HybridCache(2, D, 0, DI, n_blocks=8, max_blocks=4, device=DEV, idx_fmt=fmt)
+    tail = torch.randn((128, D), generator=g, device=DEV).to(torch.bfloat16)
+    ents = torch.zeros((64, 2 * D), dtype=torch.uint8, device=DEV)
+    keys = torch.randn((128, DI), generator=g, device=DEV).to(torch.bfloat16)
+    for b in range(2):
+        hc.load_prefix(b, tail, tail, 256, ents)
+    i = torch.arange(64, dtype=torch.int32, device=DEV)
+    proj = pipeline.QueryProjection((torch.randn((HI * DI, K), generator=g, device=DEV) / 16).to(torch.bfloat16), HI, DI,
+                                    max_q=2, fmt=fmt)
+    q_seq, q_pos = i[:2].clone(), torch.full((2,), 255, dtype=torch.int32, device=DEV)
+    w = torch.rand((2, HI), generator=g, device=DEV)
+    qI, qs = proj(_hidden(g, 2), q_pos)
+    idx = torch.full((2, 16), -1, dtype=torch.int32, device=DEV)
+    ws = torch.empty(L.csa_indexer_workspace_size(2, 64, 16), dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    select = lambda s=None: hc.select(qI, qs, w, q_seq, q_pos, idx, H_I=HI, k=16, workspace=ws, stream=s)  # noqa: E731
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(5_000_000)
+        seq = torch.zeros_like(i) + 1
+    hc.append_keys((seq, i), keys[64:], stream=side)
+    with pytest.raises(RuntimeError, match="sequence 0"):
+        select(side)
+    hc.append_keys((torch.zeros_like(i), i), keys[:64])
+    torch.cuda.synchronize()
+    select()
+    want = idx.clone()
+    items = torch.cat([torch.zeros_like(i), seq]), torch.cat([i, i])
+    for b in range(2):
+        hc.load_prefix(b, tail, tail, 256, ents)
+    hc.kI.zero_()
+    idx.fill_(-1)
+    graph = torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        hc.append_keys(items, keys)
+        select()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(idx, want) and int(hc.dev_status.item()) == 0
+    select()
+    assert torch.equal(idx, want)
