@@ -66,9 +66,11 @@ class HybridCache:
     def __init__(self, B: int, D: int, fmt: int, d_I: int, n_blocks: int, max_blocks: int,
                  ring: int = 128, device="cuda", idx_fmt: int = CSA_IDX_FP8):
         """idx_fmt: the key store's rows, CSA_IDX_FP8 (kI e4m3, ks fp32) or CSA_IDX_MXFP4
-        (kI packed e2m1, ks UE8M0 bytes)."""
+        (kI packed e2m1, ks UE8M0 bytes; d_I = 128, as its indexer takes)."""
         if idx_fmt not in (CSA_IDX_FP8, CSA_IDX_MXFP4):
             raise ValueError(f"unknown indexer format {idx_fmt}")
+        if idx_fmt == CSA_IDX_MXFP4 and d_I != 128:
+            raise ValueError(f"the MXFP4 indexer reads keys of 128 channels, not {d_I}")
         self.B, self.D, self.fmt, self.d_I, self.ring = B, D, fmt, d_I, ring
         self.idx_fmt = idx_fmt
         dev = torch.device(device)

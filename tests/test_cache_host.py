@@ -140,3 +140,11 @@ def test_select_refuses_a_prefix_and_a_reused_sequence_without_keys(calls):
         hc.append(kv, kv, torch.zeros((2, 128), dtype=torch.uint8), torch.ones(2))
     select()
     assert hc._unkeyed == [0, 0]
+
+
+def test_a_store_that_no_indexer_reads_is_refused():
+    # the MXFP4 indexer takes 128 channels only: the cache says so when it is made, not in select
+    with pytest.raises(ValueError, match="128 channels, not 64"):
+        cache.HybridCache(1, 128, 0, 64, n_blocks=2, max_blocks=2, device="cpu", idx_fmt=L.CSA_IDX_MXFP4)
+    for d, f in ((64, L.CSA_IDX_FP8), (128, L.CSA_IDX_FP8), (128, L.CSA_IDX_MXFP4)):
+        cache.HybridCache(1, 128, 0, d, n_blocks=2, max_blocks=2, device="cpu", idx_fmt=f)
