@@ -308,7 +308,8 @@ __device__ __noinline__ RowCodes quantize_row_f64(const Lane x, const float* wei
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 const double z = y[c][j] * inv;
-                f[j] = f64_to_f32_odd(bad ? 0.0 : fma(fma(-z, sd, y[c][j]), inv, z));
+                // a zero keeps its sign, which its remainder would lose
+                f[j] = f64_to_f32_odd(bad ? 0.0 : z == 0.0 ? z : fma(fma(-z, sd, y[c][j]), inv, z));
             }
             const uint2 q = pack_e4m3x8(f);
             o.c[c][0] = q.x;

@@ -785,3 +785,21 @@ def test_append_through_a_slice_of_a_block_table(fmt, compiled, monkeypatch):
     codes[row], scale[row] = 0x11, scale[(row + 1) % 768]
     blank = _store(fmt, (24 * 32,), 128)
     assert torch.equal(codes, blank[0]) and torch.equal(scale, blank[1])
+
+
+@pytest.mark.parametrize("fmt", [L.CSA_IDX_FP8, L.CSA_IDX_MXFP4])
+@pytest.mark.parametrize("rope", [0, 64, 128])
+def test_zeros_keep_their_sign(rope, fmt):
+    # zeros of both signs (channels, and pairs of them, which a rotation turns into either) in enough
+    # rows that many are settled in fp64
+    g = torch.Generator(device=DEV).manual_seed(rope + 1)
+    x = torch.randn((200, 16, 128), generator=g, device=DEV)
+    drop = torch.rand((200, 16, 64, 1), generator=g, device=DEV) < 0.2
+    x = torch.where(drop, torch.copysign(torch.zeros_like(x), x).unflatten(2, (64, 2)), x.unflatten(2, (64, 2))).flatten(2)
+    x[:, :, 5] = -0.0
+    pos = torch.randint(0, 1 << 20, (200,), generator=g, device=DEV, dtype=torch.int32)
+    codes, scale = _store(fmt, (200, 16), 128)
+    st = _status()
+    L.csa_indexer_queries(x, pos, codes, scale, fmt=fmt, rope_dims=rope, dev_status=st)
+    _sync(st)
+    _same(codes, scale, _quant_ref(io.norm_rope(f64(x), pos.cpu().numpy(), rope=rope), fmt))
