@@ -198,10 +198,15 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const QkArgs 
 // 64 x 128: 72 -> 68 us; MXFP4 sends 1 in 200 either way).  With rows' sums of squares below
 // 2^100, weights below 2^40 and results within 2^-60 .. 2^100 nothing overflows, and an
 // underflowed product is below 2^-34 of a quotient's unit, far from every border but zero's,
-// whose sign it keeps.
+// whose sign it keeps without a rotation.  Where every product is zero in fp32 (values below 2^-148),
+// the norm may lift them back: a block then counts as zero if the mean square is above 2^-36,
+// which leaves them below 2^-130, an eighth of the least scale; a row in e4m3, whose scales reach
+// down to 2^-149, only if its inputs are zeros.  (Both tests on every row: 8192 tokens of 64 x 128
+// to MXFP4 50.6 -> 51.7 us.)
 constexpr float kU24 = 5.9604645e-08f;
 constexpr float kAbsMargin = 5.f * kU24, kRelMargin = 15.f * kU24, kTopMargin = 24.f * kU24;
 constexpr float kTiny = 8.6736174e-19f, kHuge = 1.2676506e+30f;   // 2^-60, 2^100
+constexpr float kLeastMean = 1.4551915e-11f;                      // 2^-36
 
 struct RowQuant {
     uint8_t* codes;    // rows of D (e4m3) or D / 2 (e2m1) bytes
@@ -393,6 +398,14 @@ __device__ __forceinline__ void bracket(const float* v, const float* mag, bool r
     }
 }
 
+// Whether any of a chunk's inputs is not a zero.
+__device__ __forceinline__ bool any_nonzero(const float* x) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int j = 0; j < 8; j++) bits |= __float_as_uint(x[j]);
+    return (bits & 0x7fffffffu) != 0u;
+}
+
 // One row over LPR = D / 16 lanes (all lanes of the warp call it): norm, rotation, codes and
 // scale.  codes, scale: this lane's first word and its row's scales.
 template <int LPR, bool FP4, RotMode RM>
@@ -408,7 +421,7 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
     const float ss = group_sum<LPR>((s[0][0] + s[0][1]) + (s[1][0] + s[1][1]));   // NaNs and infinities show here
     near |= !(ss < kHuge);
     const float ms = fmaf(ss, 1.f / D, eps);
-    near |= norm & !(ms > kTiny);
+    near |= norm & !(ms > (FP4 ? kLeastMean : kTiny));
     const float r = norm ? rsqrtf(ms) : 1.f;
     Lane v;
     float mag[kC][4], amax[kC];      // of a rotated pair: |v1| + |v2| before the rotation
@@ -436,6 +449,7 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
         for (int j = 0; j < 8; j++) amax[c] = fmaxf(amax[c], fabsf(v.v[c][j]));
     }
     RowCodes q;
+    bool blank = false;          // e4m3: every product of the row is zero
     if constexpr (FP4) {
 #pragma unroll
         for (int c = 0; c < kC; c++) {
@@ -465,6 +479,7 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
         for (int m = 1; m < LPR; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
         const bool zero = top == 0.f;
         near |= !zero & (!(fminf(top, top * r) > kTiny) | !(top * r < kHuge));
+        blank = zero;
         const float inv = zero ? 1.f : 448.f / top;
 #pragma unroll
         for (int c = 0; c < kC; c++) {
@@ -478,14 +493,20 @@ __device__ __forceinline__ void quantize_row(const Lane& x, int l, const LanePar
             near |= !zero & ((a.x != b.x) | (a.y != b.y));
         }
     }
-    const unsigned unsettled = __ballot_sync(0xffffffffu, near);
+    unsigned unsettled = __ballot_sync(0xffffffffu, near | blank);
     if (unsettled) {
-        const RowCodes d = quantize_row_f64<LPR, FP4>(x, p.weight, p.rot(0), p.rot(1), norm, (double)eps);
-        // by row: the fp32 scale of a settled neighbour may differ from the fp64 one in its
-        // last bits, and a row's result must not depend on the rows beside it
-        if (unsettled >> ((threadIdx.x & 31) & ~(LPR - 1)) & ((1u << LPR) - 1u)) {
-            q = d;
-            if (in && ((FP4 ? l & 3 : l) == 0) && (q.bad[0] | q.bad[1])) flag(st, CSA_DEV_NAN);
+        if constexpr (!FP4) {
+            if (blank) near |= any_nonzero(x.v[0]) | any_nonzero(x.v[1]);
+            unsettled = __ballot_sync(0xffffffffu, near);
+        }
+        if (unsettled) {
+            const RowCodes d = quantize_row_f64<LPR, FP4>(x, p.weight, p.rot(0), p.rot(1), norm, (double)eps);
+            // by row: the fp32 scale of a settled neighbour may differ from the fp64 one in its
+            // last bits, and a row's result must not depend on the rows beside it
+            if (unsettled >> ((threadIdx.x & 31) & ~(LPR - 1)) & ((1u << LPR) - 1u)) {
+                q = d;
+                if (in && ((FP4 ? l & 3 : l) == 0) && (q.bad[0] | q.bad[1])) flag(st, CSA_DEV_NAN);
+            }
         }
     }
     if (!in) return;

@@ -803,3 +803,87 @@ def test_zeros_keep_their_sign(rope, fmt):
     L.csa_indexer_queries(x, pos, codes, scale, fmt=fmt, rope_dims=rope, dev_status=st)
     _sync(st)
     _same(codes, scale, _quant_ref(io.norm_rope(f64(x), pos.cpu().numpy(), rope=rope), fmt))
+
+
+@pytest.mark.parametrize("fmt", [L.CSA_IDX_FP8, L.CSA_IDX_MXFP4])
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("D,rope", [(64, 0), (64, 32), (64, 64), (128, 0), (128, 32), (128, 64), (128, 128)])
+def test_ties_and_their_neighbours_on_every_kernel(D, rope, dt, fmt):
+    # values on the borders between codes, and in fp32 one step to either side, which no bracket settles:
+    # without the norm, at position 0 (no angle), in every kernel.  Zero blocks and rows among them
+    rng = np.random.default_rng(D + rope + fmt)
+    if fmt == L.CSA_IDX_MXFP4:
+        v, top, one = (io.LEVELS[1:] + io.LEVELS[:-1]) / 2, 6.0, 32
+    else:
+        codes = np.arange(127, dtype=np.uint8).view(io.ml_dtypes.float8_e4m3fn).astype(np.float64)
+        v, top, one = (codes[1:] + codes[:-1]) / 2, 448.0, D
+    rows = rng.choice(v[v >= 2.0 ** -6], (300, 2, D)) * rng.choice([-1, 1], (300, 2, D))
+    if dt == "f32":
+        rows *= 1 + rng.integers(-1, 2, rows.shape) * 2.0 ** -23
+    rows.reshape(-1, one)[:, 0] = top                    # the scale is the row's power of two
+    rows.reshape(-1, one)[::7] = 0
+    rows *= 2.0 ** rng.integers(-6, 7, (300, 2, 1))
+    x = _gpu(rows.astype(np.float32), DT[dt])
+    assert dt != "bf16" or np.array_equal(f64(x), rows)  # borders stay borders
+    pos = torch.zeros(300, dtype=torch.int32, device=DEV)
+    codes, scale = _store(fmt, (300, 2), D)
+    st = _status()
+    L.csa_indexer_queries(x, pos, codes, scale, fmt=fmt, norm=False, rope_dims=rope, dev_status=st)
+    _sync(st)
+    _same(codes, scale, _quant_ref(f64(x), fmt))
+    # and as keys: entry 0 of its sequence, one token long, stands at position 0
+    kc, ks = _store(fmt, (300,), D)
+    b = torch.arange(300, dtype=torch.int32, device=DEV)
+    L.csa_indexer_append(x[:, 1], torch.ones(300, dtype=torch.int64, device=DEV), b.long(), b, torch.zeros_like(b), kc, ks,
+                         B=300, m=1, fmt=fmt, norm=False, rope_dims=rope, dev_status=st)
+    _sync(st)
+    _same(kc, ks, _quant_ref(f64(x[:, 1]), fmt))
+
+
+def _unsigned_zeros(packed):
+    """Packed e2m1 codes with -0 as 0."""
+    packed = packed * (packed & 0x0f != 8) | packed * (packed & 0x0f == 8) & 0xf0
+    return packed * (packed & 0xf0 != 0x80) | packed * (packed & 0xf0 == 0x80) & 0x0f
+
+
+@pytest.mark.parametrize("fmt", [L.CSA_IDX_FP8, L.CSA_IDX_MXFP4])
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("rope", [0, 64])
+def test_rows_whose_products_underflow_are_not_zero_rows(rope, norm, fmt):
+    # products x * weight below fp32's least, while the norm lifts the rows to 2^-121 and their
+    # scales into range: whole rows (FP8's zero test) and blocks (MXFP4's), beside rows of true
+    # zeros, and rows that only a weight of zero empties.  The sign of a zero code is the definition's
+    # but where rotated products underflow in an MXFP4 block (which stays on the fp32 path)
+    x = torch.zeros((8, 4, 128), device=DEV)
+    sign = 1 - 2 * (torch.arange(128, device=DEV) % 3 == 1).float()
+    small = sign * torch.linspace(1.0, 1.5, 128, device=DEV) * 2.0 ** -90
+    x[1], x[1, :, 0] = small, 2.0 ** -26
+    x[2, :, 32:64], x[2, :, 0] = small[32:64], 2.0 ** -26
+    x[3, 1:3, 96:], x[3, 1:3, 0] = small[96:], 2.0 ** -26
+    x[4] = small * 2.0 ** -50
+    x[5, :, 0] = 3.0
+    x[6, :, 1:] = torch.randn(127, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)
+    x[7, 2] = small
+    w = torch.full((128,), 2.0 ** -61, device=DEV)
+    w[0] = 0
+    pos = torch.arange(8, dtype=torch.int32, device=DEV) * 1001
+    for eps in (0.0, 1e-30, 1e-6):
+        # (a row of zeros has no norm without an eps)
+        keep = [1, 2, 4, 5, 6] if norm and eps == 0.0 else list(range(8))
+        q, p = x[keep].contiguous(), pos[keep].contiguous()
+        codes, scale = _store(fmt, q.shape[:2], 128)
+        st = _status()
+        L.csa_indexer_queries(q, p, codes, scale, fmt=fmt, weight=w, norm=norm, rope_dims=rope, eps=eps, dev_status=st)
+        _sync(st)
+        ref = _quant_ref(io.norm_rope(f64(q), p.cpu().numpy(), f64(w), norm=norm, rope=rope, eps=eps), fmt)
+        lax = _unsigned_zeros if rope and fmt == L.CSA_IDX_MXFP4 else (lambda c: c)  # noqa: E731
+        _same(lax(codes), scale, (lax(ref[0]), ref[1]))
+        kc, ks = _store(fmt, (8,), 128)
+        item = torch.arange(len(keep), dtype=torch.int32, device=DEV)
+        L.csa_indexer_append(q[:, 1], torch.tensor([400], device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV),
+                             torch.zeros_like(item), item, kc, ks, B=1, fmt=fmt, weight=w, norm=norm, rope_dims=rope,
+                             eps=eps, dev_status=st)
+        _sync(st)
+        y = io.norm_rope(f64(q[:, 1:2]), np.arange(len(keep)) * 4 + 3, f64(w), norm=norm, rope=rope, eps=eps)
+        ref = _quant_ref(y[:, 0], fmt)
+        _same(lax(kc[:len(keep)]), ks[:len(keep)], (lax(ref[0]), ref[1]))
