@@ -287,22 +287,17 @@ __device__ __noinline__ RowCodes quantize_row_f64(const Lane x, const float* wei
             o.bad[c] = bad;
         }
     } else {
-        double top = 0.0;
-        bool nan = false;
+        // magnitudes compare as integers, a NaN above an infinity above the rest
+        unsigned long long top = 0;
 #pragma unroll
         for (int c = 0; c < kC; c++)
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                top = fmax(top, fabs(y[c][j]));
-                nan |= y[c][j] != y[c][j];
-            }
+            for (int j = 0; j < 8; j++)
+                top = max(top, (unsigned long long)__double_as_longlong(fabs(y[c][j])));
 #pragma unroll
-        for (int s = LPR / 2; s > 0; s >>= 1) {
-            top = fmax(top, __shfl_xor_sync(0xffffffffu, top, s));
-            nan |= __shfl_xor_sync(0xffffffffu, (int)nan, s) != 0;
-        }
-        float scale = (float)(top / 448.0);
-        const bool bad = nan || !(scale <= 3.402823466e38f);
+        for (int s = LPR / 2; s > 0; s >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
+        float scale = (float)(__longlong_as_double((long long)top) / 448.0);
+        const bool bad = !(scale <= 3.402823466e38f);
         if (!(scale > 0.f) || bad) scale = 1.f;
         // y / scale: the product with the rounded reciprocal, mended once by its remainder, so
         // that a quotient fp64 holds (a tie between two codes, say) comes out exactly
@@ -313,8 +308,8 @@ __device__ __noinline__ RowCodes quantize_row_f64(const Lane x, const float* wei
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 const double z = y[c][j] * inv;
-                // a zero keeps its sign, which its remainder would lose
-                f[j] = f64_to_f32_odd(bad ? 0.0 : z == 0.0 ? z : fma(fma(-z, sd, y[c][j]), inv, z));
+                // (a zero's remainder would lose its sign)
+                f[j] = f64_to_f32_odd(bad ? 0.0 : fma(fma(-z, sd, y[c][j]), inv, z), bad ? 0.0 : z);
             }
             const uint2 q = pack_e4m3x8(f);
             o.c[c][0] = q.x;

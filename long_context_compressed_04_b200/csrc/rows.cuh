@@ -159,14 +159,17 @@ __device__ __forceinline__ void fma2(float* d, const float* a, const float* b, c
 // result to a format of at most 21 fraction bits gives what rounding z itself gives.
 // Magnitudes below 2^-126 come back as one just above it (for the formats here both round to
 // zero); |z| must be below 2^128.
-__device__ __forceinline__ float f64_to_f32_odd(double z) {
+// The sign is that of `sign`.
+__device__ __forceinline__ float f64_to_f32_odd(double z, double sign) {
     const uint32_t hi = (uint32_t)__double2hiint(z), lo = (uint32_t)__double2loint(z);
+    const uint32_t neg = (uint32_t)__double2hiint(sign) & 0x80000000u;
     const uint32_t mag = hi & 0x7fffffffu;
     const bool small = mag < (897u << 20);
     const uint32_t a = (small ? (897u << 20) : mag) - (896u << 20);
     uint32_t f = __funnelshift_l(lo, a, 3);
     f |= (lo & 0x1fffffffu) ? 1u : 0u;
-    return __uint_as_float(z == 0.0 ? (hi & 0x80000000u) : (f | (hi & 0x80000000u)));
+    return __uint_as_float(z == 0.0 ? neg : (f | neg));
 }
+__device__ __forceinline__ float f64_to_f32_odd(double z) { return f64_to_f32_odd(z, z); }
 
 }  // namespace csa
