@@ -12,6 +12,8 @@
 // each.  8192 tokens of 64 + 1 heads x 128 in bf16 (273 MB): norm and rotation 50 us, 5.4 TB/s,
 // bound by HBM; query heads to MXFP4 (170 MB) 50 us, to FP8 (203 MB) 68, bound by instructions
 // (256 per lane and 16 channels for MXFP4, half of them the scale, the brackets and the codes).
+#include <type_traits>
+
 #include "launchers.cuh"
 #include "rows.cuh"
 
@@ -63,6 +65,71 @@ __device__ __forceinline__ void load_weight8(const float* weight, int ch, float*
     }
 }
 
+// Its two top bits are 0 if a mean square lies in 2^-64 .. 2^64; beyond, squares of the row may have
+// left fp32's range.  (Bits of several may be joined.)
+__device__ __forceinline__ uint32_t range_bits(float ms) { return __float_as_uint(ms) - (63u << 23); }
+
+// Mean of a row's squares over its lanes, plus eps.
+template <int LPR, int C>
+__device__ __forceinline__ float mean_square(const float (&f)[C][8], float inv_d, float eps) {
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            s0 = fmaf(f[c][j], f[c][j], s0);
+            s1 = fmaf(f[c][j + 1], f[c][j + 1], s1);
+        }
+    return fmaf(group_sum<LPR>(s0 + s1), inv_d, eps);
+}
+
+// Rows whose squares leave fp32's range (all lanes of the warp call it): a row whose mean square lies
+// outside 2^-64 .. 2^64 is multiplied by the power of two that brings the larger of its greatest
+// magnitude and sqrt(eps) near 1, which its norm undoes.  Rows in range keep their bits.
+template <int LPR, int C>
+__device__ __forceinline__ float rescaled_mean_square(float (&f)[C][8], float ms, float inv_d, float eps) {
+    float top = sqrtf(eps);
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+        for (int j = 0; j < 8; j++) top = fmaxf(top, fabsf(f[c][j]));
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -120), 120);
+    const float k = range_bits(ms) >> 30 == 0u ? 1.f : __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+        for (int j = 0; j < 8; j++) f[c][j] *= k;
+    return mean_square<LPR, C>(f, inv_d, eps * k * k);
+}
+
+// A row's values, normed by rs, weighted and rotated, into its output.
+template <class T, int LPR, int C>
+__device__ __forceinline__ void finish_row(float (&f)[C][8], float rs, const float (&w)[C][8], const float (&cs)[C][4],
+                                           const float (&sn)[C][4], int D, int lo, int l, T* dst, bool write) {
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+        const int ch = 8 * (l + LPR * c);
+#pragma unroll
+        for (int j = 0; j < 8; j++) f[c][j] *= rs * w[c][j];
+        if (ch + 8 > lo) {
+#pragma unroll
+            for (int p = 0; p < 4; p++) {
+                const float a = f[c][2 * p], b = f[c][2 * p + 1];
+                // a chunk may hold the border: its first pairs stay as they are
+                if (ch >= lo || ch + 2 * p >= lo) {
+                    f[c][2 * p] = a * cs[c][p] - b * sn[c][p];
+                    f[c][2 * p + 1] = a * sn[c][p] + b * cs[c][p];
+                }
+            }
+        }
+        Row8<T> o;
+        o.set(f[c]);
+        if (write && ch < D) o.store(dst + 8 * LPR * c);
+    }
+}
+
 // Heads [h0, h1) of one token, kU passes of 32 / LPR rows at a time: the loads of all kU go
 // out before the first is used.
 template <class T, int LPR, int C, int kU>
@@ -70,6 +137,7 @@ __device__ __forceinline__ void norm_rope_heads(const QkRows& x, int64_t t, int 
                                                 int lo, bool norm, float eps, int sub, int l,
                                                 const float (&cs)[C][4], const float (&sn)[C][4]) {
     constexpr int kRows = 32 / LPR;
+    constexpr bool kRanged = !std::is_same<T, __half>::value;     // fp16's squares stay in range
     float w[C][8];
 #pragma unroll
     for (int c = 0; c < C; c++) {
@@ -84,50 +152,66 @@ __device__ __forceinline__ void norm_rope_heads(const QkRows& x, int64_t t, int 
         Row8<T> r[kU][C];
         // lanes past the last head load the last one again: no zeroing, no predicate
         const bool full = hb + kU * kRows <= h1;
-#pragma unroll
-        for (int u = 0; u < kU; u++) {
+        const auto load = [&](Row8<T>(&row)[C], int u) {
             const T* from = src + u * step;
             if (!full) from -= max(hb + sub + u * kRows - (h1 - 1), 0) * x.sh;
 #pragma unroll
             for (int c = 0; c < C; c++)
-                if (8 * (l + LPR * c) < D) r[u][c].load(from + 8 * LPR * c);
-        }
-#pragma unroll
-        for (int u = 0; u < kU; u++) {
-            float f[C][8];
-            float s0 = 0.f, s1 = 0.f;
+                if (8 * (l + LPR * c) < D) row[c].load(from + 8 * LPR * c);
+        };
+        const auto values = [&](Row8<T>(&row)[C], float(&f)[C][8]) {
 #pragma unroll
             for (int c = 0; c < C; c++) {
-                if (8 * (l + LPR * c) >= D) r[u][c].zero();
-                r[u][c].get(f[c]);
-#pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    s0 = fmaf(f[c][j], f[c][j], s0);
-                    s1 = fmaf(f[c][j + 1], f[c][j + 1], s1);
-                }
+                if (8 * (l + LPR * c) >= D) row[c].zero();
+                row[c].get(f[c]);
             }
+        };
+#pragma unroll
+        for (int u = 0; u < kU; u++) load(r[u], u);
+        if constexpr (kU == 1) {
+            float f[C][8];
+            values(r[0], f);
             float rs = 1.f;
-            if (norm) rs = rsqrtf(fmaf(group_sum<LPR>(s0 + s1), inv_d, eps));
-            const bool in = full | (hb + sub + u * kRows < h1);
+            if (norm) {
+                float ms = mean_square<LPR, C>(f, inv_d, eps);
+                if (kRanged && __any_sync(0xffffffffu, range_bits(ms) >> 30))
+                    ms = rescaled_mean_square<LPR, C>(f, ms, inv_d, eps);
+                rs = rsqrtf(ms);
+            }
+            finish_row<T, LPR, C>(f, rs, w, cs, sn, D, lo, l, dst, full | (hb + sub < h1));
+        } else {
+            // every mean square before the first row is done: one test of their range and the
+            // shuffles of all kU in flight (4096 tokens of 33 heads x 64 in bf16 10.8 -> 9.0 us)
+            float ms[kU];
+            uint32_t far = 0;
 #pragma unroll
-            for (int c = 0; c < C; c++) {
-                const int ch = 8 * (l + LPR * c);
-#pragma unroll
-                for (int j = 0; j < 8; j++) f[c][j] *= rs * w[c][j];
-                if (ch + 8 > lo) {
-#pragma unroll
-                    for (int p = 0; p < 4; p++) {
-                        const float a = f[c][2 * p], b = f[c][2 * p + 1];
-                        // a chunk may hold the border: its first pairs stay as they are
-                        if (ch >= lo || ch + 2 * p >= lo) {
-                            f[c][2 * p] = a * cs[c][p] - b * sn[c][p];
-                            f[c][2 * p + 1] = a * sn[c][p] + b * cs[c][p];
-                        }
-                    }
+            for (int u = 0; u < kU; u++) {
+                float f[C][8];
+                values(r[u], f);
+                ms[u] = norm ? mean_square<LPR, C>(f, inv_d, eps) : 1.f;
+                far |= range_bits(ms[u]);
+            }
+            if (kRanged && __any_sync(0xffffffffu, far >> 30)) {
+                // from the inputs again (nothing of these rows is written yet), and not unrolled: it
+                // costs the others no registers
+#pragma unroll 1
+                for (int u = 0; u < kU; u++) {
+                    Row8<T> row[C];
+                    float f[C][8];
+                    load(row, u);
+                    values(row, f);
+                    const float m = rescaled_mean_square<LPR, C>(f, mean_square<LPR, C>(f, inv_d, eps), inv_d, eps);
+                    finish_row<T, LPR, C>(f, rsqrtf(m), w, cs, sn, D, lo, l, dst + u * ostep,
+                                          hb + sub + u * kRows < h1);
                 }
-                Row8<T> o;
-                o.set(f[c]);
-                if (in && ch < D) o.store(dst + u * ostep + 8 * LPR * c);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kU; u++) {
+                    float f[C][8];
+                    values(r[u], f);
+                    finish_row<T, LPR, C>(f, norm ? rsqrtf(ms[u]) : 1.f, w, cs, sn, D, lo, l, dst + u * ostep,
+                                          full | (hb + sub + u * kRows < h1));
+                }
             }
         }
         src += kU * step;
@@ -135,9 +219,16 @@ __device__ __forceinline__ void norm_rope_heads(const QkRows& x, int64_t t, int 
     }
 }
 
+// Resident CTAs that the registers have to allow: what the kernels took before their rows' range was
+// tested, without which 8192 x 65 x 128 took 50.5 us instead of 49.6.
+template <class T, int C>
+constexpr int qk_blocks() {
+    return sizeof(T) == 2 ? (C == 1 ? 7 : C == 2 ? 5 : 4) : (C == 1 ? 5 : C <= 3 ? 4 : 3);
+}
+
 // LPR lanes a row, C chunks of 8 channels a lane (chunk c of lane l: channels 8 (l + LPR c)).
 template <class T, int LPR, int C>
-__global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const QkArgs a, const RopeTable rt) {
+__global__ void __launch_bounds__(32 * kWarps, qk_blocks<T, C>()) qk_norm_rope_kernel(const QkArgs a, const RopeTable rt) {
     pdl_wait();
     const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
     const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -167,7 +258,8 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const QkArgs 
             sn[c][p] = r.y;
         }
     }
-    constexpr int kU = C == 1 ? 4 : C == 2 ? 2 : 1;
+    // (four rows of fp32 in flight per lane: 4096 x 65 x 128 55 us against 50 with one)
+    constexpr int kU = sizeof(T) == 4 ? 1 : C == 1 ? 4 : C == 2 ? 2 : 1;
     if (h0 < a.q.heads)
         norm_rope_heads<T, LPR, C, kU>(a.q, t, h0, min(h1, a.q.heads), a.D, lo, a.norm, a.eps, sub, l, cs, sn);
     if (h1 > a.q.heads)

@@ -887,3 +887,40 @@ def test_rows_whose_products_underflow_are_not_zero_rows(rope, norm, fmt):
         y = io.norm_rope(f64(q[:, 1:2]), np.arange(len(keep)) * 4 + 3, f64(w), norm=norm, rope=rope, eps=eps)
         ref = _quant_ref(y[:, 0], fmt)
         _same(lax(kc[:len(keep)]), ks[:len(keep)], (lax(ref[0]), ref[1]))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-6])
+@pytest.mark.parametrize("H,D,rope", [(9, 64, 64), (6, 128, 64), (5, 256, 32), (5, 512, 0), (4, 576, 64), (3, 1024, 128)])
+def test_qk_norm_rope_past_the_range_of_fp32_squares(H, D, rope, eps, dt):
+    # rows whose squares overflow or underflow fp32, whole or in their largest element only, beside
+    # ordinary ones, whose results have the bits of a call without the others
+    g = torch.Generator(device=DEV).manual_seed(D)
+    x = torch.randn((12, H, D), generator=g, device=DEV)
+    plain = x.to(DT[dt])
+    for t, s in ((1, 1e25), (2, 1e-25), (3, 2.0 ** 120), (4, 2.0 ** -120), (6, 1e19), (7, 1e-19)):
+        x[t, 1 - t % 2::2] *= s
+    x[8, 0, 7] = 3e38
+    x[9, 1] *= 1e-38
+    x[9, 1, -1] = 1e-20
+    x[10] *= 1e-40
+    x = x.to(DT[dt])
+    same = (x == plain).all(-1)
+    pos = torch.randint(0, 1 << 20, (12,), generator=g, device=DEV, dtype=torch.int32)
+    w = 1 + 0.2 * torch.randn(D, generator=g, device=DEV)
+    out, ref, kout = (torch.empty_like(x) for _ in range(3))
+    L.csa_qk_norm_rope(x, x, pos, out, kout, q_weight=w, k_weight=w, rope_dims=rope, eps=eps)
+    L.csa_qk_norm_rope(plain, None, pos, ref, None, q_weight=w, rope_dims=rope, eps=eps)
+    torch.cuda.synchronize()
+    assert torch.equal(out[same], ref[same]) and torch.equal(out, kout)
+    y = io.norm_rope(f64(x), pos.cpu().numpy(), f64(w), rope=rope, eps=eps)
+    # the bound of the fp32 path, whose magnitudes are those of the normed row without a rotation
+    n = (8 * -(-D // 256) + 6) / 2 + 13
+    mag = np.abs(io.norm_rope(f64(x), 0, f64(w), rope=0, eps=eps))
+    if rope:
+        pair = mag[..., D - rope::2] + mag[..., D - rope + 1::2]
+        mag[..., D - rope:] = np.repeat(pair, 2, -1)
+    fi = torch.finfo(DT[dt])
+    bound = n * 2.0 ** -24 * mag + np.abs(y) * fi.eps / 2 * (1 + 1e-3) + fi.tiny * fi.eps
+    err = np.abs(f64(out) - y)
+    assert np.all(err <= bound), (err / bound).max()
