@@ -924,3 +924,55 @@ def test_qk_norm_rope_past_the_range_of_fp32_squares(H, D, rope, eps, dt):
     bound = n * 2.0 ** -24 * mag + np.abs(y) * fi.eps / 2 * (1 + 1e-3) + fi.tiny * fi.eps
     err = np.abs(f64(out) - y)
     assert np.all(err <= bound), (err / bound).max()
+
+
+def _feature_tile(M, N, K):
+    """The features per tile that the library takes for more than 96 tokens: the least cost of rounds
+    over the SMs (the rule and its constants stand at launch_mxfp4_matmul)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    nk = -(-K // 256)
+    cost = {ct: -(-(-(-M // 128) * -(-N // ct)) // sms) * (fixed + stage * nk)
+            for ct, fixed, stage in ((256, 160, 41), (128, 70, 28), (64, 45, 27))}
+    return min(cost, key=lambda ct: (cost[ct], -ct))
+
+
+# (M, N, K) of every feature tile: N past a tile by less and by more than half of it, whole and ragged K
+_TILES = [(700, 5000, 1504, 256), (1900, 2100, 1504, 256), (450, 5003, 736, 256), (2000, 2200, 1536, 256),
+          (300, 5000, 1504, 128), (1300, 3330, 800, 128), (900, 4999, 1248, 128), (515, 1300, 2048, 64)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M,N,K,ct", _TILES)
+def test_matmul_every_feature_tile_bit_exact(M, N, K, ct, dt):
+    # exact sums; rows of the output that the TMA unit stores (whole 16-byte pieces) and others
+    if torch.cuda.get_device_properties(0).multi_processor_count == 148:
+        assert _feature_tile(M, N, K) == ct
+    rng = np.random.default_rng(M + N)
+    a, b = _operands(rng, M, N, K, 126, 127)
+    want = torch.from_numpy(a[2] @ b[2].T).to(DT[dt])
+    for pad in (0, 3, 8 + -N % 8):
+        out = torch.full((M + 2, N + pad), 3.0, dtype=DT[dt], device=DEV)
+        st = _status()
+        L.csa_mxfp4_matmul(_gpu(a[0]), _gpu(io.tile_scales(a[1])), _gpu(b[0]), _gpu(io.tile_scales(b[1])), out[:M, :N],
+                           dev_status=st)
+        _sync(st)
+        assert torch.equal(out[:M, :N].cpu(), want), pad
+        assert bool((out[:M, N:] == 3.0).all()) and bool((out[M:] == 3.0).all()), pad
+
+
+@pytest.mark.parametrize("M,N,K,ct", [t for t in _TILES if t[3] > 64])
+def test_matmul_rows_do_not_depend_on_the_feature_tile(M, N, K, ct):
+    # wide block exponents, so that the order of the additions shows: the same rows in batches of the
+    # few-token kernel's widths and of narrower tiles, and the same features of narrower weights
+    rng = np.random.default_rng(M + N + 1)
+    a, b = _operands(rng, M, N, K, 115, 139)
+    full = _matmul(a, b, "f32")
+    bits = lambda t: t.contiguous().view(torch.int32)  # noqa: E731
+    for lo, n in [(0, 1), (M - 17, 17), (5, 65), (130, 97), (M - 128, 128)]:
+        part = _matmul([x[lo:lo + n] for x in a], b, "f32")
+        assert torch.equal(bits(part), bits(full[lo:lo + n])), (lo, n)
+    for lo, n in [(0, 100), (128, 32), (N - 260, 260), (N - 7, 7), (256, 700)]:
+        part = _matmul(a, [x[lo:lo + n] for x in b], "f32")
+        assert torch.equal(bits(part), bits(full[:, lo:lo + n])), (lo, n)
+    for dt in ("bf16", "f16"):
+        assert torch.equal(_matmul(a, b, dt), full.to(DT[dt]))
