@@ -53,11 +53,13 @@ class BlockAllocator:
 class Items(tuple):
     """(item_seq, item_ent) of entries on the device, with the same as host lists."""
 
-    def __new__(cls, seqs: List[int], ents: List[int], device):
-        self = super().__new__(cls, (torch.tensor(seqs, dtype=torch.int32, device=device),
-                                     torch.tensor(ents, dtype=torch.int32, device=device)))
-        self.host = (seqs, ents)
+    def __new__(cls, tensors, host):
+        self = super().__new__(cls, tensors)
+        self.host = host
         return self
+
+    def __getnewargs__(self):
+        return tuple(self), self.host
 
 
 class HybridCache:
@@ -221,7 +223,8 @@ class HybridCache:
                 ents.append(i)
                 self._keyed[b][i] = kI_new is not None
                 self._unkeyed[b] += kI_new is None
-        return Items(seqs, ents, self.device)
+        return Items((torch.tensor(seqs, dtype=torch.int32, device=self.device),
+                      torch.tensor(ents, dtype=torch.int32, device=self.device)), (seqs, ents))
 
     def append_keys(self, items, k, weight=None, norm: bool = True, rope_dims: int = 64,
                     rope_theta=10000.0, eps=1e-6, stream=None):

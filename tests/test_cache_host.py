@@ -1,6 +1,8 @@
 """Host-side bookkeeping of the hybrid cache (no GPU): the block free list, block-table growth
 as entries complete, release, and the layout struct handed to the C calls."""
+import copy
 import ctypes
+import pickle
 
 import pytest
 import torch
@@ -148,3 +150,12 @@ def test_a_store_that_no_indexer_reads_is_refused():
         cache.HybridCache(1, 128, 0, 64, n_blocks=2, max_blocks=2, device="cpu", idx_fmt=L.CSA_IDX_MXFP4)
     for d, f in ((64, L.CSA_IDX_FP8), (128, L.CSA_IDX_FP8), (128, L.CSA_IDX_MXFP4)):
         cache.HybridCache(1, 128, 0, d, n_blocks=2, max_blocks=2, device="cpu", idx_fmt=f)
+
+
+def test_item_lists_are_tuples_that_can_be_copied(calls):
+    hc, kv, _ = _decode_cache(L.CSA_IDX_FP8)
+    for _ in range(4):
+        items = hc.append(kv, kv)
+    seq, ent = items
+    for c in (copy.copy(items), copy.deepcopy(items), pickle.loads(pickle.dumps(items))):
+        assert torch.equal(c[0], seq) and torch.equal(c[1], ent) and c.host == ([0, 1], [0, 0])
