@@ -331,14 +331,15 @@ __device__ __noinline__ RowCodes quantize_row_f64(const Lane x, const float* wei
                                                   const double2* rot1, bool norm, double eps) {
     constexpr int D = 8 * kC * LPR;
     double y[kC][8];
-    double ss = 0.0;
+    double s4[4] = {};         // four chains: a call's time is that of its dependent instructions
 #pragma unroll
     for (int c = 0; c < kC; c++)
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             y[c][j] = (double)x.v[c][j];
-            ss = fma(y[c][j], y[c][j], ss);
+            s4[j & 3] = fma(y[c][j], y[c][j], s4[j & 3]);
         }
+    const double ss = (s4[0] + s4[1]) + (s4[2] + s4[3]);
     double r = 1.0;
     if (norm) r = rsqrt(group_sum<LPR>(ss) * (1.0 / D) + eps);
 #pragma unroll
