@@ -450,8 +450,9 @@ csa_status_t lightning_indexer_topk_noalloc(const uint8_t* qI, const float* qI_s
  *   cols: a multiple of 32, up to 2^20
  *
  * csa_mxfp4_dequantize -- the values MXFP4 rows stand for, out [rows, cols] in dtype, row
- *   stride ld (exact in fp32 and bf16; fp16 rounds to nearest and overflows to infinity; a
- *   block with scale 0xFF gives NaN).
+ *   stride ld (exact in fp32 and bf16, but past their largest values, which only scale bytes
+ *   253 and 254 reach, infinity; fp16 rounds to nearest and overflows to infinity; a block
+ *   with scale 0xFF gives NaN).
  *
  * csa_mxfp4_matmul -- out[m, n] = sum_k A[m, k] B[n, k] on the tensor cores.
  *   a uint8 [M, K / 2] and b uint8 [N, K / 2] packed e2m1 (say activations and a weight),
@@ -478,7 +479,9 @@ csa_status_t csa_mxfp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uint8
  * pass ("DeepSeek-V4 深度分析报告" "其他注意力技术细节": RMSNorm of queries and KV, partial RoPE).
  *   y = x / sqrt(mean(x^2) + eps) * weight over the D channels of a head (norm = 0: y = x *
  *   weight); then the last rope_dims channels are rotated in interleaved pairs at pos[t],
- *   pair j by pos * theta^(-2j / rope_dims).  fp32 arithmetic, angles in fp64, one rounding.
+ *   pair j by pos * theta^(-2j / rope_dims).  fp32 arithmetic, angles in fp64 (off by up to
+ *   pos 2^-52), one rounding.  Rows of any finite magnitude: where the squares leave fp32's
+ *   range, the row is scaled first.
  * Arguments:
  *   q, k, q_out, k_out: [T, heads, D] in dtype, element strides *_st between tokens and *_sh
  *   between heads; q has H heads, k has Hk (either may be NULL with 0 heads).  An output may
@@ -494,10 +497,11 @@ csa_status_t csa_mxfp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uint8
  *   q [Q, H, D] in dtype (strides q_st, q_sh), q_pos int32 [Q]; codes and scale contiguous
  *   [Q, H, ..] in fmt (CSA_IDX_*; scale: fp32 [Q, H], or UE8M0 [Q, H, D / 32] bytes).
  *   D 64 or 128; rope_dims a multiple of 8, 0 .. D.  The codes and the UE8M0 scales are those
- *   of the definition in exact arithmetic (a value next to a rounding border is settled in
- *   fp64), whatever the batch; an fp32 scale is within 2^-19 of it.  A row (FP8) or
- *   block (MXFP4) that is not finite, or past the scale's range, gets a NaN scale and zero
- *   codes and sets CSA_DEV_NAN.
+ *   of the definition with the angles formed in fp64 (a value next to a rounding border is
+ *   settled in fp64), whatever the batch, for positions below 2^28; the sign of a zero code
+ *   alone may differ where products x * weight are too small for fp32 and then rotated.  An
+ *   fp32 scale is within 2^-19 of the definition's.  A row (FP8) or block (MXFP4) that is not
+ *   finite, or past the scale's range, gets a NaN scale and zero codes and sets CSA_DEV_NAN.
  *
  * csa_indexer_append -- indexer keys of listed entries into the key store.
  *   Key n (row n of k [n_items, D], row stride k_ld) belongs to entry item_ent[n] of sequence
@@ -506,7 +510,9 @@ csa_status_t csa_mxfp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uint8
  *   ..] and scale [ent_rows, ..] (block table of the layout, or ent_off).  Any number of
  *   entries per sequence, in any order; only the listed rows are written.  An entry listed
  *   twice must carry the same key.  A sequence >= B, an entry whose block has not ended
- *   ((i + 1) * m > seq_len[b]) or a row outside ent_rows sets CSA_DEV_OOB and is not written.
+ *   ((i + 1) * m > seq_len[b]), one past the block table's bt_stride blocks or a row outside
+ *   ent_rows sets CSA_DEV_OOB and is not written.  (bt_stride is taken for the table's width:
+ *   its last row is read up to there too.)
  *   csa_cache_append (kI_new = NULL) and csa_compress fill the rest of the cache.
  * Errors (all three): CSA_ERR_INVALID_ARG, CSA_ERR_UNSUPPORTED, CSA_ERR_CUDA.
  */

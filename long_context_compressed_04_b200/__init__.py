@@ -576,7 +576,8 @@ def csa_qk_norm_rope(q, k, pos, q_out, k_out, *, q_weight=None, k_weight=None, n
                      stream=None):
     """RMSNorm of the query heads q [T, H, D] and key heads k [T, Hk, D] (either may be None)
     and rotation of their last rope_dims channels at pos (int32 [T]), in one launch.  An
-    output may be its own input."""
+    output may be its own input.  sparse_mqa_attn and dense_hca_attn rotate their queries
+    themselves: rope_dims=0 makes their input, the default would have them rotated twice."""
     if _marshal is not None:
         status = _marshal.qk_norm_rope(q, k, pos, q_out, k_out, q_weight, k_weight, norm, rope_dims,
                                        rope_theta, eps, _handle(stream))

@@ -251,7 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // take the accumulator into registers at once (CT / 2 columns a thread) and hand it back, so
 // the next tile's MMAs wait for those loads only; the conversion, a 2 KB transposition per warp
 // in shared memory and the stores of 64 contiguous bytes a row (TMA where rows allow) run beside
-// them.  8192 x 8192 x 2048 to bf16: 65 us, 4.2 PFLOP/s; without the stores 50, whose traffic
+// them.  8192 x 8192 x 2048 to bf16: 66 us, 4.2 PFLOP/s, at 1965 MHz (bursts of 100 calls); 77 us in a
+// loop, which the power cap holds at 1590 MHz and 987 W.  Without the stores 50, whose traffic
 // (134 MB) competes with the operands' loads; 5.5 PFLOP/s per further stage.  Tried and slower:
 // two accumulators of 192 columns (75 us), scales written to TMEM by four warps instead of
 // copies in the MMA warp's stream (71), streaming stores (69), features fastest (71).

@@ -10,8 +10,9 @@
 // the whole row stays in registers between its one load and its one store; a warp walks rows
 // (heads) that share a position, whose cosines and sines its lanes form once, in fp64, a pair
 // each.  8192 tokens of 64 + 1 heads x 128 in bf16 (273 MB): norm and rotation 50 us, 5.4 TB/s,
-// bound by HBM; query heads to MXFP4 (170 MB) 50 us, to FP8 (203 MB) 68, bound by instructions
-// (256 per lane and 16 channels for MXFP4, half of them the scale, the brackets and the codes).
+// bound by HBM; query heads to MXFP4 (170 MB) 50 us, to FP8 (203 MB) 62, bound by instructions
+// (256 per lane and 16 channels for MXFP4, half of them the scale, the brackets and the codes; FP8
+// converts two values of a bracket to each code and has more passes in fp64).
 #include <type_traits>
 
 #include "launchers.cuh"
@@ -286,8 +287,10 @@ __global__ void __launch_bounds__(32 * kWarps, qk_blocks<T, C>()) qk_norm_rope_k
 //   e4m3: z = v * (448 / max|v|), from which r drops out: 8 u of the largest |v|, u each of the
 //   division, the product, the definition's rounding of the scale to fp32: 11 u.
 // The bracket's own roundings add 2 u.  Counted whole against |v1| + |v2|, the bound of e4m3, whose
-// codes are dense near zero, sent 1 pass in 15 to fp64, where this sends 1 in 38 (8192 tokens of
-// 64 x 128: 72 -> 68 us; MXFP4 sends 1 in 200 either way).  With rows' sums of squares below
+// codes are dense near zero, sent 1 pass in 15 to fp64, where this sends 1 in 38 (4 us of 72 for 8192
+// tokens of 64 x 128 with a random weight; MXFP4 sends 1 in 200 either way; bf16 rows without a
+// weight lie on borders more often).  The angle's own error, pos 2^-52 of |v1| + |v2|, finds u of
+// room in the bound: positions below 2^28.  With rows' sums of squares below
 // 2^100, weights below 2^40 and results within 2^-60 .. 2^100 nothing overflows, and an
 // underflowed product is below 2^-34 of a quotient's unit, far from every border but zero's,
 // whose sign it keeps without a rotation.  Where every product is zero in fp32 (values below 2^-148),
