@@ -976,3 +976,24 @@ def test_matmul_rows_do_not_depend_on_the_feature_tile(M, N, K, ct):
         assert torch.equal(bits(part), bits(full[:, lo:lo + n])), (lo, n)
     for dt in ("bf16", "f16"):
         assert torch.equal(_matmul(a, b, dt), full.to(DT[dt]))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,D", [(3, 70, 128), (2, 131, 64), (3, 37, 320), (2, 5, 1024), (2000, 9, 128)])
+def test_qk_norm_rope_past_the_range_in_place(T, H, D, dt):
+    # rows that are done again from their inputs, in place and strided, here and there among many heads
+    g = torch.Generator(device=DEV).manual_seed(H)
+    x = torch.randn((T, H * D + 64), generator=g, device=DEV)
+    scale = torch.tensor([1.0, 1.0, 1.0, 1e24, 1e-24], device=DEV)
+    pick = torch.randint(0, 5, (T, H), generator=g, device=DEV)
+    x[:, :H * D] *= scale[pick].repeat_interleave(D, 1)
+    x = x.to(DT[dt])
+    q, tail = x[:, :H * D].unflatten(1, (H, D)), x[:, H * D:].clone()
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device=DEV, dtype=torch.int32)
+    out, want = torch.empty((T, H, D), dtype=x.dtype, device=DEV), io.norm_rope(f64(q), pos.cpu().numpy(), rope=64, eps=0.0)
+    L.csa_qk_norm_rope(q, None, pos, out, None, eps=0.0)
+    L.csa_qk_norm_rope(q, None, pos, q, None, eps=0.0)
+    torch.cuda.synchronize()
+    assert torch.equal(q, out) and torch.equal(x[:, H * D:], tail)
+    # pairs of normed magnitude below 64: 2^-24 of it some twenty times, and half a step of the type
+    assert np.all(np.abs(f64(out) - want) <= 64 * 30 * 2.0 ** -24 + np.abs(want) * torch.finfo(x.dtype).eps / 2 * 1.001)
